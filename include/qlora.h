@@ -283,6 +283,115 @@ QLORA_API qlora_status qlora_rmsnorm_bwd(const qlora_bf16* X, const qlora_bf16* 
                                          const qlora_bf16* dY, int64_t M, int64_t d, int32_t plus_one,
                                          qlora_bf16* dX, qlora_stream_t stream);
 
+/* ------------------------------------------------------------- 8-bit ----
+ * e4m3 codes (one byte each, fp8 with 4 exponent and 3 mantissa bits, largest
+ * value 448) with fp32 scales: a value is code * scale.
+ * Rows [M, K]: codes [M, K], scale [ceil(K / 128), M], one per 128 consecutive
+ * columns of a row (scale[b * M + m] belongs to columns [128 b, 128 b + 128) of
+ * row m). */
+typedef struct {
+  uint8_t* codes;
+  float* scale;
+} qlora_fp8_rows;
+
+/* Weight [n_out, k_in]: codes [n_out, k_in], scale
+ * [ceil(n_out / 128), ceil(k_in / 128)], one per 128 x 128 block. */
+typedef struct {
+  const uint8_t* codes;
+  const float* scale;
+  int64_t n_out;
+  int64_t k_in;
+} qlora_fp8;
+
+/* One projection with a frozen e4m3 base weight plus its LoRA adapter. */
+typedef struct {
+  qlora_fp8 w;
+  const qlora_bf16* A;
+  const qlora_bf16* B;
+  int32_t r;   /* 16, 32 or 64 */
+  float scale; /* s = alpha / r (or any scale) */
+} qlora_lora_linear8;
+
+/* Quantisation to the two formats.  With amax the largest magnitude of a block,
+ * scale is the smallest power of two s >= 2^-126 with amax / s <= 448 and code =
+ * e4m3(v / s), rounded to nearest even: dividing by a power of two is exact, so
+ * the result is the same bit for bit in any implementation.  A NaN takes no part
+ * in amax and keeps its place; a block that holds an infinity gets an infinite
+ * scale and stands for NaN throughout.
+ * Rows: K % 8 == 0.  Weight: k_in % 16 == 0, n_out % 16 == 0. */
+QLORA_API qlora_status fp8_quantize_rows(const qlora_bf16* X, int64_t M, int64_t K, uint8_t* codes, float* scale,
+                                         qlora_stream_t stream);
+QLORA_API qlora_status fp8_quantize(const qlora_bf16* w, int64_t n_out, int64_t k_in, uint8_t* codes, float* scale,
+                                    qlora_stream_t stream);
+
+/* Block-scaled products of 8-bit operands:
+ *   fp8_matmul:    Y  = x W^T  from x  [M, k_in]  -> Y  [M, n_out]
+ *   fp8_matmul_t:  dX = dY W   from dY [M, n_out] -> dX [M, k_in]
+ * with the values the codes and scales stand for, any finite fp32 scales (not
+ * only the quantisers' powers of two), fp32 sums and one rounding to bf16.  A NaN
+ * or infinite value in a row of x makes that row of the output NaN or infinite
+ * and touches no other row.  k_in % 16 == 0, n_out % 16 == 0. */
+QLORA_API size_t fp8_matmul_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out);
+QLORA_API qlora_status fp8_matmul(const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* Y,
+                                  void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+QLORA_API qlora_status fp8_matmul_t(const qlora_fp8_rows* dY, const qlora_fp8* w, int64_t M, qlora_bf16* dX,
+                                    void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/* LoRA projection over an e4m3 base, forward and backward, as qlora_linear_fwd
+ * and qlora_linear_bwd with both dense products in 8 bits:
+ *   XA = X A                                  -> XA_saved [M, r]
+ *   Y  = q(X) W^T + s XA B                    -> Y [M, n_out]
+ *   dX = q(dY) W + s (dY B^T) A^T,  dA = s X^T (dY B^T),  dB = s XA^T dY
+ * q(.) is fp8_quantize_rows; the adapter's terms read the bf16 X and dY.  X8 is
+ * X already quantised (qlora_add_rmsnorm_fwd writes it), or NULL: the call then
+ * quantises X in its workspace.  k_in % 16 == 0, n_out % 16 == 0, r = 16, 32 or
+ * 64. */
+QLORA_API size_t qlora_linear8_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out, int32_t r);
+QLORA_API qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* X, const qlora_fp8_rows* X8,
+                                         int64_t M, qlora_bf16* Y, qlora_bf16* XA_saved, void* workspace,
+                                         size_t workspace_bytes, qlora_stream_t stream);
+QLORA_API qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* X,
+                                         const qlora_bf16* XA_saved, const qlora_bf16* dY, int64_t M, qlora_bf16* dX,
+                                         qlora_bf16* dA, qlora_bf16* dB, void* workspace, size_t workspace_bytes,
+                                         qlora_stream_t stream);
+
+/* Residual addition and RMS norm in one pass (the step in front of a projection):
+ *   H = bf16(X + R),  rstd = 1 / sqrt(mean_j H_j^2 + eps),  Y = H * rstd * g,
+ *   Y8 = fp8_quantize_rows(Y),  g = w or 1 + w as qlora_rmsnorm_fwd.
+ * R and H may both be NULL (H is then X itself); one of Y and Y8 may be NULL.
+ * H may be X or R (in place).  The sum of squares is held in binary64. d % 8 == 0. */
+QLORA_API qlora_status qlora_add_rmsnorm_fwd(const qlora_bf16* X, const qlora_bf16* R, const qlora_bf16* w, int64_t M,
+                                             int64_t d, float eps, int32_t plus_one, qlora_bf16* H, qlora_bf16* Y,
+                                             const qlora_fp8_rows* Y8, float* rstd, qlora_stream_t stream);
+/* Its backward with the norm weight frozen:
+ *   dX = dH + rstd * (g * dY - n * mean_j(n_j g_j dY_j)),  n = H * rstd,
+ * the gradient of X and of R alike.  dH [M, d] is the gradient that reaches H
+ * past the norm (NULL: none).  dX may be dY or dH (in place). */
+QLORA_API qlora_status qlora_add_rmsnorm_bwd(const qlora_bf16* H, const qlora_bf16* w, const float* rstd,
+                                             const qlora_bf16* dY, const qlora_bf16* dH, int64_t M, int64_t d,
+                                             int32_t plus_one, qlora_bf16* dX, qlora_stream_t stream);
+
+/* Rotary positions on the heads of X [M, heads * head_dim] (row stride ldx
+ * elements), e.g. the q and k columns of a fused Q/K/V output:
+ *   (a, b) -> factor * (a cos t - b sin t, b cos t + a sin t),
+ *   t = 2 pi * position * turns[i] / 2^64,
+ * for the pairs i < rot / 2 of each head: (2i, 2i + 1) if interleaved, else
+ * (i, i + rot / 2).  The elements from rot on are copied (left alone in place).
+ * turns [rot / 2] holds each pair's frequency in turns per position as a 64-bit
+ * fraction; the angle is exact to 2^-34 turns at position 2^31.  positions [M]
+ * (8-byte aligned), or NULL: row m has position m % seq_len (m if seq_len is 0).
+ * out [M, heads * head_dim] with row stride ldo; it is X itself with ldo = ldx (in
+ * place) or does not overlap X.  The backward is the transposed rotation of dY.
+ * head_dim % 8 == 0 and <= 512, rot even, ldx % 8 == 0, ldo % 8 == 0. */
+QLORA_API qlora_status qlora_rope_fwd(const qlora_bf16* X, int64_t M, int64_t ldx, int32_t heads, int32_t head_dim,
+                                      const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,
+                                      const int64_t* positions, int64_t seq_len, qlora_bf16* out, int64_t ldo,
+                                      qlora_stream_t stream);
+QLORA_API qlora_status qlora_rope_bwd(const qlora_bf16* dY, int64_t M, int64_t ldy, int32_t heads, int32_t head_dim,
+                                      const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,
+                                      const int64_t* positions, int64_t seq_len, qlora_bf16* dX, int64_t ldx,
+                                      qlora_stream_t stream);
+
 /* Reads the device status word in `workspace` (synchronising `stream`),
  * clears it, and maps it to a status: QLORA_OK, QLORA_ERR_TIMEOUT or
  * QLORA_ERR_DEVICE. */

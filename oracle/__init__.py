@@ -45,11 +45,12 @@ from .lora import (ACTIVATIONS, act_fwd, act_grad, linear_bwd, linear_fwd,
                    mlp_bwd, mlp_fwd)
 from .cost import bracket_costs, bracket_speedup_limit
 from .norm import rmsnorm_bwd, rmsnorm_fwd
+from . import fp8, rope
 
 __all__ = [
     "bf16_bits_to_f64", "f32_to_bf16_bits", "f64_to_f32",
     "NF4_BLOCK", "nf4_codebook", "nf4_midpoints", "nf4_quantize",
     "nf4_quantize_bruteforce", "nf4_dequantize",
     "ACTIVATIONS", "act_fwd", "act_grad", "linear_fwd", "linear_bwd",
-    "mlp_fwd", "mlp_bwd", "bracket_costs", "bracket_speedup_limit", "rmsnorm_fwd", "rmsnorm_bwd",
+    "mlp_fwd", "mlp_bwd", "bracket_costs", "bracket_speedup_limit", "rmsnorm_fwd", "rmsnorm_bwd", "fp8", "rope",
 ]

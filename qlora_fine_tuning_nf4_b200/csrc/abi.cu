@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <vector>
 
@@ -37,6 +38,17 @@ cudaError_t launch_rmsnorm_fwd(const bf16* X, const bf16* w, int M, int d, float
                                float* rstd, cudaStream_t st);
 cudaError_t launch_rmsnorm_bwd(const bf16* X, const bf16* w, const float* rstd, const bf16* dY, int M, int d,
                                int plus_one, bf16* dX, cudaStream_t st);
+cudaError_t launch_add_rmsnorm_fwd(const bf16* X, const bf16* R, const bf16* w, int M, int d, float eps, int plus_one,
+                                   bf16* H, bf16* Y, uint8_t* codes, float* scale, float* rstd, cudaStream_t st);
+cudaError_t launch_add_rmsnorm_bwd(const bf16* H, const bf16* w, const float* rstd, const bf16* dY, const bf16* dH,
+                                   int M, int d, int plus_one, bf16* dX, cudaStream_t st);
+cudaError_t launch_fp8_quantize_rows(const bf16* X, int64_t M, int64_t K, uint8_t* codes, float* scale,
+                                     cudaStream_t st);
+cudaError_t launch_fp8_quantize(const bf16* w, int64_t N, int64_t K, uint8_t* codes, float* scale, cudaStream_t st);
+cudaError_t launch_gemm_fp8(bool bwd, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
+cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
+                        bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
+                        int64_t ldo, cudaStream_t st);
 extern const uint32_t h_nf4_bits[16];
 int g_grid_cap = 0;
 }  // namespace ql
@@ -48,11 +60,13 @@ namespace {
 // ------------------------------------------------------------- tracing ---
 enum KernelId : int {
   K_QUANT = 0, K_DEQUANT, K_GEMM_FWD, K_GEMM_GLU_FWD, K_GEMM_BWD, K_GEMM_GLU_BWD, K_ROWPROJ, K_COLPROJ, K_DYPASS,
-  K_REDUCE, K_NORM_FWD, K_NORM_BWD, K_COUNT
+  K_REDUCE, K_NORM_FWD, K_NORM_BWD, K_ADDNORM_FWD, K_ADDNORM_BWD, K_FP8_ROWS, K_FP8_QUANT, K_GEMM8_FWD, K_GEMM8_BWD,
+  K_ROPE, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "gemm_nf4_fwd", "gemm_nf4_gateup_glu_fwd", "gemm_nf4_bwd_dx",
-    "gemm_nf4_down_bwd_glu", "skinny_rowproj", "skinny_colproj", "skinny_dypass", "skinny_reduce", "rmsnorm_fwd", "rmsnorm_bwd"};
+    "gemm_nf4_down_bwd_glu", "skinny_rowproj", "skinny_colproj", "skinny_dypass", "skinny_reduce", "rmsnorm_fwd", "rmsnorm_bwd",
+    "add_rmsnorm_fwd", "add_rmsnorm_bwd", "fp8_quantize_rows", "fp8_quantize", "gemm_fp8_fwd", "gemm_fp8_bwd_dx", "rope"};
 
 std::atomic<uint64_t> g_launches{0};
 bool g_trace = false;
@@ -1312,6 +1326,284 @@ qlora_status qlora_rmsnorm_bwd(const qlora_bf16* X, const qlora_bf16* w, const f
   return cuda_status(launch_rmsnorm_bwd(reinterpret_cast<const bf16*>(X), reinterpret_cast<const bf16*>(w), rstd,
                                         reinterpret_cast<const bf16*>(dY), (int)M, (int)d, plus_one ? 1 : 0,
                                         reinterpret_cast<bf16*>(dX), st));
+}
+
+// ------------------------------------------------- residual add + norm ----
+qlora_status qlora_add_rmsnorm_fwd(const qlora_bf16* X, const qlora_bf16* R, const qlora_bf16* w, int64_t M, int64_t d,
+                                   float eps, int32_t plus_one, qlora_bf16* H, qlora_bf16* Y,
+                                   const qlora_fp8_rows* Y8, float* rstd, qlora_stream_t stream) {
+  if (M < 0 || d <= 0 || !(eps >= 0.f)) return QLORA_ERR_INVALID_ARG;
+  if (d % 8 || d > kMaxDim || M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!X || !w || !rstd || (!R != !H) || (!Y && !Y8)) return QLORA_ERR_INVALID_ARG;
+  if (Y8 && (!Y8->codes || !Y8->scale)) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(X) || misaligned(R) || misaligned(w) || misaligned(H) || misaligned(Y) || misaligned(rstd) ||
+      (Y8 && (misaligned(Y8->codes) || misaligned(Y8->scale))))
+    return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  KScope k(K_ADDNORM_FWD, st);
+  return cuda_status(launch_add_rmsnorm_fwd(
+      reinterpret_cast<const bf16*>(X), reinterpret_cast<const bf16*>(R), reinterpret_cast<const bf16*>(w), (int)M,
+      (int)d, eps, plus_one ? 1 : 0, reinterpret_cast<bf16*>(H), reinterpret_cast<bf16*>(Y), Y8 ? Y8->codes : nullptr,
+      Y8 ? Y8->scale : nullptr, rstd, st));
+}
+
+qlora_status qlora_add_rmsnorm_bwd(const qlora_bf16* H, const qlora_bf16* w, const float* rstd, const qlora_bf16* dY,
+                                   const qlora_bf16* dH, int64_t M, int64_t d, int32_t plus_one, qlora_bf16* dX,
+                                   qlora_stream_t stream) {
+  if (M < 0 || d <= 0) return QLORA_ERR_INVALID_ARG;
+  if (d % 8 || d > kMaxDim || M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!H || !w || !rstd || !dY || !dX) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(H) || misaligned(w) || misaligned(rstd) || misaligned(dY) || misaligned(dH) || misaligned(dX))
+    return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  KScope k(K_ADDNORM_BWD, st);
+  return cuda_status(launch_add_rmsnorm_bwd(reinterpret_cast<const bf16*>(H), reinterpret_cast<const bf16*>(w), rstd,
+                                            reinterpret_cast<const bf16*>(dY), reinterpret_cast<const bf16*>(dH),
+                                            (int)M, (int)d, plus_one ? 1 : 0, reinterpret_cast<bf16*>(dX), st));
+}
+
+// ---------------------------------------------------------------- rope ----
+static qlora_status rope(const qlora_bf16* X, int64_t M, int64_t ldx, int32_t heads, int32_t head_dim,
+                         const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,
+                         const int64_t* positions, int64_t seq_len, qlora_bf16* out, int64_t ldo, bool transpose,
+                         qlora_stream_t stream) {
+  if (M < 0 || heads <= 0 || head_dim <= 0 || rot <= 0 || rot > head_dim || seq_len < 0 || !std::isfinite(factor))
+    return QLORA_ERR_INVALID_ARG;
+  const int64_t cols = static_cast<int64_t>(heads) * head_dim;
+  if (ldx < cols || ldo < cols) return QLORA_ERR_INVALID_ARG;
+  if (head_dim % 8 || head_dim > 512 || rot % 2 || ldx % 8 || ldo % 8 || M > kMaxDim || cols > kMaxDim ||
+      ldx > kMaxDim || ldo > kMaxDim)
+    return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!X || !turns || !out || (X == out && ldx != ldo)) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(X) || misaligned(turns) || misaligned(out) || (reinterpret_cast<uintptr_t>(positions) & 7u))
+    return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  KScope k(K_ROPE, st);
+  return cuda_status(launch_rope(reinterpret_cast<const bf16*>(X), M, ldx, heads, head_dim, turns, rot,
+                                 interleaved != 0, factor, transpose, positions, seq_len, reinterpret_cast<bf16*>(out),
+                                 ldo, st));
+}
+qlora_status qlora_rope_fwd(const qlora_bf16* X, int64_t M, int64_t ldx, int32_t heads, int32_t head_dim,
+                            const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,
+                            const int64_t* positions, int64_t seq_len, qlora_bf16* out, int64_t ldo,
+                            qlora_stream_t stream) {
+  return rope(X, M, ldx, heads, head_dim, turns, rot, interleaved, factor, positions, seq_len, out, ldo, false, stream);
+}
+qlora_status qlora_rope_bwd(const qlora_bf16* dY, int64_t M, int64_t ldy, int32_t heads, int32_t head_dim,
+                            const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,
+                            const int64_t* positions, int64_t seq_len, qlora_bf16* dX, int64_t ldx,
+                            qlora_stream_t stream) {
+  return rope(dY, M, ldy, heads, head_dim, turns, rot, interleaved, factor, positions, seq_len, dX, ldx, true, stream);
+}
+
+// ----------------------------------------------------------------- fp8 ----
+qlora_status fp8_quantize_rows(const qlora_bf16* X, int64_t M, int64_t K, uint8_t* codes, float* scale,
+                               qlora_stream_t stream) {
+  if (M < 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
+  if (K % 8 || M > kMaxDim || K > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (cdiv(K, 256) * cdiv(M, 32) > INT32_MAX) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!X || !codes || !scale) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(X) || misaligned(codes) || misaligned(scale)) return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  KScope k(K_FP8_ROWS, st);
+  return cuda_status(launch_fp8_quantize_rows(reinterpret_cast<const bf16*>(X), M, K, codes, scale, st));
+}
+
+qlora_status fp8_quantize(const qlora_bf16* w, int64_t n_out, int64_t k_in, uint8_t* codes, float* scale,
+                          qlora_stream_t stream) {
+  if (n_out <= 0 || k_in <= 0) return QLORA_ERR_INVALID_ARG;
+  if (k_in % 16 || n_out % 16 || n_out > kMaxDim || k_in > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (cdiv(k_in, 128) * cdiv(n_out, 128) > INT32_MAX) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (!w || !codes || !scale) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(w) || misaligned(codes) || misaligned(scale)) return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  KScope k(K_FP8_QUANT, st);
+  return cuda_status(launch_fp8_quantize(reinterpret_cast<const bf16*>(w), n_out, k_in, codes, scale, st));
+}
+
+namespace {
+qlora_status check_fp8(const qlora_fp8* w) {
+  if (!w || !w->codes || !w->scale || w->n_out <= 0 || w->k_in <= 0) return QLORA_ERR_INVALID_ARG;
+  if (w->k_in % 16 || w->n_out % 16) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (w->k_in > kMaxDim || w->n_out > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  // the GEMM counts 128 x 128 weight blocks in 32-bit integers
+  if (cdiv(w->k_in, 128) * cdiv(w->n_out, 128) > INT32_MAX) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (misaligned(w->codes) || misaligned(w->scale)) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+// D = x W^T (bwd = false) or x W, plus L Rt with the LoRA operands L [M, r] and B [r, n_out] or
+// A [k_in, r] (r = 0: none).
+qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const qlora_fp8& w, int64_t M, bf16* D,
+                      const bf16* L, const bf16* Rf, int r, int* status, cudaStream_t st) {
+  const int64_t K = w.k_in, N = w.n_out;
+  const int64_t red = bwd ? N : K, out = bwd ? K : N;
+  Gemm8Maps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!make_map(&maps.a, u8, 1, codes, red, M, red, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.b, u8, 1, w.codes, K, N, K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map_bf16(&maps.out, D, out, M, out, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return QLORA_ERR_CUDA;
+  if (r > 0 && (!map_bf16(&maps.la, L, r, M, r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                !(bwd ? map_bf16(&maps.lb, Rf, r, K, r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)
+                      : map_bf16(&maps.lb, Rf, N, r, N, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))))
+    return QLORA_ERR_CUDA;
+  Gemm8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.M = (int)M;
+  a.N = (int)out;
+  a.nkb = (int)cdiv(red, 128);
+  a.lora_k16 = r / 16;
+  a.sa = scale;
+  a.sb = w.scale;
+  const int wkb = (int)cdiv(K, 128);  // the weight's scales are [ceil(n_out / 128), ceil(k_in / 128)]
+  a.sb_k = bwd ? wkb : 1;
+  a.sb_n = bwd ? 1 : wkb;
+  a.status = status;
+  a.group_m = kGroupM;
+  KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
+  return cuda_status(launch_gemm_fp8(bwd, maps, a, st));
+}
+
+qlora_status fp8_matmul_any(bool bwd, const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* out,
+                            void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  const qlora_status s = check_fp8(w);
+  if (s != QLORA_OK) return s;
+  if (M < 0) return QLORA_ERR_INVALID_ARG;
+  if (M == 0) return QLORA_OK;
+  if (!x || !x->codes || !x->scale || !out || !ws) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(x->codes) || misaligned(x->scale) || misaligned(out) || misaligned(ws)) return QLORA_ERR_MISALIGNED;
+  if (M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < fp8_matmul_workspace_bytes(M, w->k_in, w->n_out)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  return gemm_fp8(bwd, x->codes, x->scale, *w, M, reinterpret_cast<bf16*>(out), nullptr, nullptr, 0,
+                  static_cast<int*>(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+size_t fp8_matmul_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out) {
+  (void)M, (void)k_in, (void)n_out;
+  return 256;
+}
+qlora_status fp8_matmul(const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* Y, void* ws,
+                        size_t ws_bytes, qlora_stream_t stream) {
+  return fp8_matmul_any(false, x, w, M, Y, ws, ws_bytes, stream);
+}
+qlora_status fp8_matmul_t(const qlora_fp8_rows* dY, const qlora_fp8* w, int64_t M, qlora_bf16* dX, void* ws,
+                          size_t ws_bytes, qlora_stream_t stream) {
+  return fp8_matmul_any(true, dY, w, M, dX, ws, ws_bytes, stream);
+}
+
+namespace {
+// Workspace of an e4m3 projection: [status word | 256 B][M x r vector][row codes][row scales][partials]
+struct Linear8Ws {
+  size_t vec, codes, scale, part, total;
+};
+Linear8Ws linear8_ws(int64_t M, int64_t K, int64_t N, int r) {
+  Linear8Ws w;
+  const int64_t wide = std::max(K, N);
+  w.vec = 256;
+  w.codes = w.vec + align256(static_cast<size_t>(M) * r * 2);
+  w.scale = w.codes + align256(static_cast<size_t>(M) * wide);
+  w.part = w.scale + align256(static_cast<size_t>(M) * cdiv(wide, 128) * 4);
+  size_t part = rowproj_part_bytes(M, K, r);
+  part = std::max(part, dypass_part_bytes(M, N, r));
+  part = std::max(part, colproj_part_bytes(M, K, r));
+  w.total = w.part + align256(part);
+  return w;
+}
+qlora_status check_linear8(const qlora_lora_linear8* lin) {
+  if (!lin || !lin->A || !lin->B) return QLORA_ERR_INVALID_ARG;
+  const qlora_status s = check_fp8(&lin->w);
+  if (s != QLORA_OK) return s;
+  if (!rank_ok(lin->r, 4)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (misaligned(lin->A) || misaligned(lin->B)) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+}  // namespace
+
+size_t qlora_linear8_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (M <= 0 || K <= 0 || N <= 0 || !rank_ok(r, 4)) return 256;
+  return linear8_ws(M, K, N, r).total;
+}
+
+qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* X, const qlora_fp8_rows* X8, int64_t M,
+                               qlora_bf16* Y, qlora_bf16* XA_saved, void* ws, size_t ws_bytes,
+                               qlora_stream_t stream) {
+  qlora_status s = check_linear8(lin);
+  if (s != QLORA_OK) return s;
+  if (M < 0) return QLORA_ERR_INVALID_ARG;
+  if (M == 0) return QLORA_OK;
+  if (!X || !Y || !XA_saved || !ws || (X8 && (!X8->codes || !X8->scale))) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(X) || misaligned(Y) || misaligned(XA_saved) || misaligned(ws) ||
+      (X8 && (misaligned(X8->codes) || misaligned(X8->scale))))
+    return QLORA_ERR_MISALIGNED;
+  if (M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  const int64_t K = lin->w.k_in, N = lin->w.n_out;
+  const int r = lin->r;
+  const Linear8Ws l = linear8_ws(M, K, N, r);
+  if (ws_bytes < l.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  int* status = reinterpret_cast<int*>(w);
+  const uint8_t* codes = X8 ? X8->codes : reinterpret_cast<uint8_t*>(w + l.codes);
+  const float* scale = X8 ? X8->scale : reinterpret_cast<float*>(w + l.scale);
+  if (!X8 && (s = fp8_quantize_rows(X, M, K, reinterpret_cast<uint8_t*>(w + l.codes),
+                                    reinterpret_cast<float*>(w + l.scale), stream)) != QLORA_OK)
+    return s;
+  bf16* xa = reinterpret_cast<bf16*>(XA_saved);
+  const bool scaled = lin->scale != 1.0f;
+  bf16* XAs = scaled ? reinterpret_cast<bf16*>(w + l.vec) : xa;
+  s = pass_rowproj(reinterpret_cast<const bf16*>(X), M, K, reinterpret_cast<const bf16*>(lin->A), nullptr, r,
+                   reinterpret_cast<float*>(w + l.part),
+                   routs(rout(xa, 0, r, r, 0, 1.f), rout(scaled ? XAs : nullptr, 0, r, r, 0, lin->scale)), status, st);
+  if (s != QLORA_OK) return s;
+  return gemm_fp8(false, codes, scale, lin->w, M, reinterpret_cast<bf16*>(Y), XAs,
+                  reinterpret_cast<const bf16*>(lin->B), r, status, st);
+}
+
+qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* X, const qlora_bf16* XA_saved,
+                               const qlora_bf16* dY, int64_t M, qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB,
+                               void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s = check_linear8(lin);
+  if (s != QLORA_OK) return s;
+  if (M < 0) return QLORA_ERR_INVALID_ARG;
+  const int64_t K = lin->w.k_in, N = lin->w.n_out;
+  const int r = lin->r;
+  if (M == 0) {
+    qlora_bf16* g[2] = {dA, dB};
+    const int64_t n[2] = {K * r, N * r};
+    return zero_adapter_grads(g, n, 2, reinterpret_cast<cudaStream_t>(stream));
+  }
+  if (!X || !XA_saved || !dY || !dX || !dA || !dB || !ws) return QLORA_ERR_INVALID_ARG;
+  if (misaligned(X) || misaligned(XA_saved) || misaligned(dY) || misaligned(dX) || misaligned(dA) || misaligned(dB) ||
+      misaligned(ws))
+    return QLORA_ERR_MISALIGNED;
+  if (M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  const Linear8Ws l = linear8_ws(M, K, N, r);
+  if (ws_bytes < l.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  int* status = reinterpret_cast<int*>(w);
+  bf16* sG = reinterpret_cast<bf16*>(w + l.vec);
+  uint8_t* codes = reinterpret_cast<uint8_t*>(w + l.codes);
+  float* scale = reinterpret_cast<float*>(w + l.scale);
+  float* part = reinterpret_cast<float*>(w + l.part);
+  const float sc = lin->scale;
+  if ((s = fp8_quantize_rows(dY, M, N, codes, scale, stream)) != QLORA_OK) return s;
+  // G = dY B^T (stored scaled), dB = s (X A)^T dY, from the unquantised dY
+  s = pass_dypass(reinterpret_cast<const bf16*>(dY), M, N, reinterpret_cast<const bf16*>(XA_saved),
+                  reinterpret_cast<const bf16*>(lin->B), r, part, routs(rout(sG, 0, r, r, 0, sc)),
+                  routs(rout(reinterpret_cast<bf16*>(dB), 0, r, (int)N, 1, sc)), status, st);
+  if (s != QLORA_OK) return s;
+  s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG, reinterpret_cast<const bf16*>(lin->A),
+               r, status, st);
+  if (s != QLORA_OK) return s;
+  return pass_colproj(reinterpret_cast<const bf16*>(X), M, K, sG, r, part,
+                      routs(rout(reinterpret_cast<bf16*>(dA), 0, r, r, 0, 1.f)), status, st);
 }
 
 // NF4 entry points: the current tile configuration.

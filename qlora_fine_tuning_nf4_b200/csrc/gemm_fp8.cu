@@ -1,0 +1,313 @@
+// Block-scaled 8-bit GEMM for sm_100a with the LoRA term in the same pass:
+//   forward  Y  = X W^T + (s X A) B     (BWD = false, reduction over k_in)
+//   dX       dX = dY W  + (s dY B^T) A^T (BWD = true, reduction over n_out)
+// X, dY and W are e4m3; X and dY carry one fp32 scale per row and 128 reduction
+// columns, W one per 128 x 128 block.  With x_kb and w_kb the codes of reduction
+// block kb,
+//   Y[m, n] = sum_kb sa[kb, m] sw[n / 128, kb] * (x_kb w_kb^T)[m, n].
+// The scales are any fp32 numbers, so they cannot ride on the tensor core's own
+// block scaling (powers of two): each block's product is an MMA group of its own
+// into a fresh TMEM accumulator, and the epilogue warps add it, scaled, to the
+// output tile they hold in registers in fp32.
+//
+// Structure (persistent; one 256 x 256 output tile at a time per CTA pair):
+//   warp 0       TMA producer: A and W tiles (128 x 128 bytes each), LoRA operands
+//   warp 1       TMEM allocation; lane 0 of the leader CTA issues tcgen05.mma
+//   warps 2-9    accumulate: TMEM -> scale -> registers; at the tile's end
+//                registers -> bf16 -> shared memory -> TMA store
+// Two TMEM accumulators of 256 columns alternate per reduction block, so the MMA
+// of one block runs while the previous one is being added.  The LoRA term is one
+// more block: bf16 operands (kind::f16) and scale 1.
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace ql {
+
+struct Gemm8Cfg {
+  static constexpr int BM = 128;    // rows per CTA
+  static constexpr int BNT = 256;   // columns per tile
+  static constexpr int BNC = 128;   // columns of W each CTA of the pair loads
+  static constexpr int BK = 128;    // reduction block: one scale, one 128-byte row
+  static constexpr int TILE = BM * BK;  // bytes of an A or W tile
+  static constexpr int S = 6;       // operand stages
+  static constexpr int OFF_A = 0;
+  static constexpr int OFF_B = OFF_A + S * TILE;
+  static constexpr int OFF_EPI = OFF_B + S * TILE;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARP0 = 2;
+  static constexpr int EPI_SLOT = 32 * 32 * 2;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_SLOT;
+  static constexpr int NBAR = 2 * S + 5;
+  static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+  static constexpr int TMEM_COLS = 512;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+template <bool BWD>
+__global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
+    gemm_fp8_kernel(const __grid_constant__ Gemm8Maps maps, const Gemm8Args args) {
+  using C = Gemm8Cfg;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  const int n_tiles = (args.N + C::BNT - 1) / C::BNT;
+  const int m_tiles = (args.M + 2 * C::BM - 1) / (2 * C::BM);
+  const int total_tiles = n_tiles * m_tiles;
+  const int cluster = blockIdx.x / 2;
+  const int clusters = gridDim.x / 2;
+  const int blocks = args.nkb + (args.lora_k16 > 0 ? 1 : 0);  // accumulator blocks per tile
+  if (!dev_check(args.M > 0 && args.N > 0 && args.nkb > 0 && args.group_m >= 1 && args.lora_k16 >= 0 &&
+                     args.lora_k16 <= 4,
+                 args.status)) {
+    grid_dep_wait();
+    return;
+  }
+
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::S + s); };
+  const uint32_t acc_full0 = bar0 + 8u * (2 * C::S);
+  const uint32_t acc_empty0 = acc_full0 + 16u;
+  const uint32_t drain_bar = acc_full0 + 32u;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sgen + C::OFF_BAR + C::NBAR * 8);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full0 + 8u * b, 1);
+      mbar_init(acc_empty0 + 8u * b, 2 * C::EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<2>(smem_u32(tmem_holder), C::TMEM_COLS);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // tiles in groups of group_m row tiles, rows fastest inside a group (as the bf16 GEMM)
+  auto tile_coords = [&](int t, int& m0, int& n0) {
+    const int gsz = args.group_m * n_tiles;
+    const int first = (t / gsz) * args.group_m;
+    const int gm = min(m_tiles - first, args.group_m);
+    const int r = t - (first / args.group_m) * gsz;
+    m0 = (first + r % gm) * 2 * C::BM + static_cast<int>(rank) * C::BM;
+    n0 = (r / gm) * C::BNT;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      bool ok = true;
+      tma_prefetch_desc(&maps.a);
+      tma_prefetch_desc(&maps.b);
+      int j = 0;
+      for (int t = cluster; t < total_tiles && ok; t += clusters) {
+        int m0, n0;
+        tile_coords(t, m0, n0);
+        const int col = n0 + static_cast<int>(rank) * C::BNC;  // this CTA's share of the tile's columns
+        for (int kb = 0; kb < blocks; ++kb, ++j) {
+          const int s = j % C::S;
+          ok = mbar_wait(empty_bar(s), ((j / C::S) & 1) ^ 1, args.status);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 4 * C::TILE);
+          const uint32_t bar = mapa_shared(full_bar(s), 0);  // both CTAs' loads complete on the leader's barrier
+          const uint32_t a = sbase + C::OFF_A + s * C::TILE, b = sbase + C::OFF_B + s * C::TILE;
+          if (kb < args.nkb) {
+            tma_load_2d_pair(a, &maps.a, bar, kb * C::BK, m0);
+            // W rows x reduction bytes (K-major), or reduction rows x output columns (MN-major)
+            if (BWD) tma_load_2d_pair(b, &maps.b, bar, col, kb * C::BK);
+            else tma_load_2d_pair(b, &maps.b, bar, kb * C::BK, col);
+          } else {
+            // LoRA operands, 64 wide with zeros beyond the rank
+            tma_load_2d_pair(a, &maps.la, bar, 0, m0);
+            if (BWD) {
+              tma_load_2d_pair(b, &maps.lb, bar, 0, col);
+            } else {
+              tma_load_2d_pair(b, &maps.lb, bar, col, 0);
+              tma_load_2d_pair(b + 8192, &maps.lb, bar, col + 64, 0);
+            }
+          }
+        }
+      }
+      if (!ok) settle_inflight();
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA -----
+    if (rank == 0 && lane == 0) {
+      bool ok = true;
+      constexpr uint32_t idesc = idesc_e4m3(2 * C::BM, C::BNT, false, BWD);
+      constexpr uint32_t idesc_lora = idesc_bf16(2 * C::BM, C::BNT, false, !BWD);
+      int j = 0;
+      for (int t = cluster; t < total_tiles && ok; t += clusters) {
+        for (int kb = 0; kb < blocks; ++kb, ++j) {
+          const int s = j % C::S, b = j & 1;
+          ok = mbar_wait(acc_empty0 + 8u * b, ((j >> 1) & 1) ^ 1, args.status) &&
+               mbar_wait(full_bar(s), (j / C::S) & 1, args.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + b * C::BNT;
+          const uint32_t as = sbase + C::OFF_A + s * C::TILE, bs = sbase + C::OFF_B + s * C::TILE;
+          if (kb < args.nkb) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {  // 32 reduction elements each
+              const uint64_t ad = smem_desc(as + kk * 32, 16, 1024, QL_SWZ_128B);
+              const uint64_t bd = BWD ? smem_desc(bs + kk * 4096, C::TILE, 1024, QL_SWZ_128B)
+                                      : smem_desc(bs + kk * 32, 16, 1024, QL_SWZ_128B);
+              umma_e4m3<2>(acc, ad, bd, idesc, kk != 0);
+            }
+          } else {
+            for (int kk = 0; kk < args.lora_k16; ++kk) {
+              const uint64_t ad = smem_desc(as + kk * 32, 16, 1024, QL_SWZ_128B);
+              const uint64_t bd = BWD ? smem_desc(bs + kk * 32, 16, 1024, QL_SWZ_128B)
+                                      : smem_desc(bs + kk * 2048, 8192, 1024, QL_SWZ_128B);
+              umma_bf16<2>(acc, ad, bd, idesc_lora, kk != 0);
+            }
+          }
+          umma_commit<2>(empty_bar(s));
+          umma_commit<2>(acc_full0 + 8u * b);
+        }
+      }
+      // let every issued MMA finish before TMEM can be released (after an error too)
+      umma_commit<2>(drain_bar);
+      mbar_drain(drain_bar, 0);
+    }
+  } else {
+    // ------------------------------------------------------ accumulate ---
+    const int ew = warp - C::EPI_WARP0;
+    const int lg = warp & 3;    // TMEM lane quadrant this warp may access
+    const int half = ew >> 2;   // its 128 columns of the tile: one weight scale per reduction block
+    const uint32_t stg = sbase + C::OFF_EPI + ew * C::EPI_SLOT;
+    uint8_t* stg_g = sgen + C::OFF_EPI + ew * C::EPI_SLOT;
+    const uint64_t pol = l2_policy_evict_first();
+    int j = 0;
+    bool ok = true;
+    for (int t = cluster; t < total_tiles && ok; t += clusters) {
+      int m0, n0;
+      tile_coords(t, m0, n0);
+      const int row = m0 + lg * 32 + lane;
+      const int nb = n0 / 128 + half;
+      const bool in = row < args.M && nb * 128 < args.N;
+      const float* sa = args.sa + row;
+      const float* sb = args.sb + static_cast<size_t>(nb) * args.sb_n;
+      auto scale_of = [&](int kb) {
+        if (kb >= args.nkb) return 1.f;
+        return in ? __ldg(sa + static_cast<size_t>(kb) * args.M) * __ldg(sb + static_cast<size_t>(kb) * args.sb_k) : 0.f;
+      };
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      float next = scale_of(0);
+      for (int kb = 0; kb < blocks; ++kb, ++j) {
+        const int b = j & 1;
+        const float sc = next;
+        if (kb + 1 < blocks) next = scale_of(kb + 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full0 + 8u * b, (j >> 1) & 1, args.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tacc = tmem + b * C::BNT + half * 128 + (static_cast<uint32_t>(lg * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld_32x32b_x32(tacc + c * 32, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], sc, acc[c * 32 + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_empty0 + 8u * b, 0));
+      }
+      if (!ok) break;
+      // 32 x 32 chunks through this warp's shared slot (64B swizzle); the TMA store clips at the edges
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (lane == 0) bulk_wait_group_read<0>();  // the previous chunk's store has read the slot
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* v = acc + c * 32 + q * 8;
+          *reinterpret_cast<uint4*>(stg_g + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&maps.out, stg, n0 + half * 128 + c * 32, m0 + lg * 32, pol);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();  // output stores complete before the CTA exits
+  }
+
+  // ------------------------------------------------------------ teardown --
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem, C::TMEM_COLS);
+  }
+}
+
+template <bool BWD>
+static cudaError_t launch_one8(const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream) {
+  using C = Gemm8Cfg;
+  auto kern = gemm_fp8_kernel<BWD>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static int resident[64] = {0};  // co-resident CTAs (even) per device
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (!resident[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    int n = sms / 2, clusters = 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms - sms % 2), 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0 && clusters < n)
+      n = clusters;
+    cudaGetLastError();
+    resident[dev] = n * 2;
+  }
+  const int total = ((args.M + 255) / 256) * ((args.N + 255) / 256);
+  const int ctas = apply_grid_cap(total * 2 < resident[dev] ? total * 2 : resident[dev], 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, maps, args);
+}
+
+cudaError_t launch_gemm_fp8(bool bwd, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream) {
+  return bwd ? launch_one8<true>(maps, args, stream) : launch_one8<false>(maps, args, stream);
+}
+
+}  // namespace ql

@@ -66,6 +66,27 @@ struct GemmArgs {
   int group_m;  // tile order: groups of group_m output-row tiles, rows fastest inside a group (>= 1)
 };
 
+// ------------------------------------------------------------- fp8 GEMM ---
+// D = A * op(W) + LoRA with e4m3 operands and fp32 scales: A has one scale per
+// row and 128 reduction columns, W one per 128 x 128 block.
+struct Gemm8Maps {
+  CUtensorMap a;    // A operand: e4m3 [M, reduction], box {128, 128}, 128B swizzle
+  CUtensorMap b;    // weight: e4m3 [n_out, k_in], box {128, 128}, 128B swizzle
+  CUtensorMap la;   // LoRA left operand s*XA or s*G: bf16 [M, r], box {64, 128}
+  CUtensorMap lb;   // LoRA right operand: B [r, N] (forward), box {64, 64}, or A [N, r] (dX), box {64, 128}
+  CUtensorMap out;  // output: bf16 [M, N], box {32, 32}, 64B swizzle
+};
+struct Gemm8Args {
+  int M, N;             // output rows and columns
+  int nkb;              // 128-wide reduction blocks
+  int lora_k16;         // 16-wide reduction steps of the LoRA operand (rank / 16), 0 = no adapter
+  const float* sa;      // [nkb, M]
+  const float* sb;      // block scales of the weight
+  int sb_k, sb_n;       // their strides per reduction block and per 128 output columns
+  int* status;          // device status word (timeouts)
+  int group_m;          // tile order, as GemmArgs
+};
+
 // --------------------------------------------------------------- skinny ---
 // Rank-r products on warp-level mma.sync.  Each skinny kernel is persistent:
 // its P CTAs split the work units (64 x 64 tiles, or 64-row x 256-column

@@ -1,0 +1,162 @@
+// Rotary positions on the heads of a row-strided matrix, forward and backward.
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * theta_i,
+// for the pairs (2i, 2i + 1) of a head (interleaved) or (i, i + rot / 2) (halves);
+// the backward is the transposed rotation, t -> -t.  Elements from rot on pass.
+//
+// Angles are fixed-point turns: theta_i / 2 pi is a 64-bit fraction, and position
+// times it modulo 2^64 is one integer multiply whose wrap-around drops the whole
+// turns exactly.  A position p is off by p 2^-65 turns at most (2^-34 at p = 2^31),
+// where a binary32 product would be off by whole radians; no 64-bit floating point
+// and no table of cosines per position is needed.
+//
+// HBM-bound.  A CTA takes a few tokens: its threads first find each token's
+// cosines and sines once (shared memory), then stream all its heads, a thread
+// keeping its pairs' factors in registers across them.
+#include "fp8.cuh"
+
+namespace ql {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_TOK = 4;       // tokens per CTA at most
+constexpr int ROPE_MAX_D = 512;   // widest head
+
+struct RopeArgs {
+  const bf16* X;
+  bf16* out;            // may be X with the same row stride
+  const uint64_t* turns;  // [rot / 2], theta_i / 2 pi in units of 2^-64 turns
+  const int64_t* pos;   // [M], or null: row (modulo seq_len if that is positive)
+  int64_t ldx, ldo, seq_len;
+  int M, heads, D, rot;
+  int tok, hsplit;      // tokens per CTA; CTAs that share a token group's heads
+  float factor, sign;   // cos and sin are multiplied by factor; sign -1: transposed
+};
+
+template <int VEC>
+struct RopeVec;
+template <> struct RopeVec<8> { using T = uint4; };
+template <> struct RopeVec<4> { using T = uint2; };
+template <> struct RopeVec<2> { using T = uint32_t; };
+template <> struct RopeVec<1> { using T = uint16_t; };
+
+template <int VEC>
+QL_DEV void rope_unpack(const typename RopeVec<VEC>::T& u, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = __uint_as_float(static_cast<uint32_t>(u) << 16);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+}
+template <int VEC>
+QL_DEV typename RopeVec<VEC>::T rope_pack(const float (&f)[VEC]) {
+  typename RopeVec<VEC>::T u;
+  if constexpr (VEC == 1) {
+    u = static_cast<uint16_t>(pack_bf16x2(f[0], 0.f));
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  }
+  return u;
+}
+
+// One head is `np` rotated items and then D - rot untouched elements in items of
+// VEC (copied where out is not X).  A rotated item is VEC pairs read as two
+// vectors (halves), or VEC / 2 pairs in one (interleaved).
+template <bool INTER, int VEC>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeArgs a) {
+  using V = typename RopeVec<VEC>::T;
+  constexpr int NP = INTER ? VEC / 2 : VEC;  // pairs per item
+  __shared__ float2 cs[ROPE_TOK * ROPE_MAX_D / 2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int half = a.rot / 2;
+  const int row0 = static_cast<int>(blockIdx.x / a.hsplit) * a.tok;
+  const int ntok = min(a.tok, a.M - row0);
+  for (int i = threadIdx.x; i < ntok * half; i += ROPE_THREADS) {
+    const int64_t row = row0 + i / half;
+    const int64_t p = a.pos ? a.pos[row] : (a.seq_len > 0 ? row % a.seq_len : row);
+    const uint64_t t = static_cast<uint64_t>(p) * a.turns[i % half];
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+    cs[i] = make_float2(c * a.factor, s * a.factor * a.sign);
+  }
+  __syncthreads();
+  const int np = half / NP;
+  const int items = np + (a.out == a.X ? 0 : (a.D - a.rot) / VEC);
+  const int lanes = min(items, ROPE_THREADS);
+  const int hl = threadIdx.x / lanes, nh = ROPE_THREADS / lanes;
+  const int h0 = static_cast<int>(blockIdx.x % a.hsplit) * nh + hl, hstep = nh * a.hsplit;
+  if (hl >= nh) return;
+  for (int v = threadIdx.x % lanes; v < items; v += lanes) {
+    for (int k = 0; k < ntok; ++k) {
+      const bf16* x = a.X + static_cast<size_t>(row0 + k) * a.ldx;
+      bf16* o = a.out + static_cast<size_t>(row0 + k) * a.ldo;
+      if (v >= np) {
+        const int e = a.rot + (v - np) * VEC;
+#pragma unroll 4
+        for (int h = h0; h < a.heads; h += hstep)
+          *reinterpret_cast<V*>(o + h * a.D + e) = *reinterpret_cast<const V*>(x + h * a.D + e);
+        continue;
+      }
+      float2 f[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) f[i] = cs[k * half + v * NP + i];
+      if constexpr (INTER) {
+#pragma unroll 4
+        for (int h = h0; h < a.heads; h += hstep) {
+          float r[VEC];
+          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + v * VEC), r);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float p = r[2 * i], q = r[2 * i + 1];
+            r[2 * i] = p * f[i].x - q * f[i].y;
+            r[2 * i + 1] = q * f[i].x + p * f[i].y;
+          }
+          *reinterpret_cast<V*>(o + h * a.D + v * VEC) = rope_pack<VEC>(r);
+        }
+      } else {
+#pragma unroll 4
+        for (int h = h0; h < a.heads; h += hstep) {
+          float p[VEC], q[VEC];
+          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + v * VEC), p);
+          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + half + v * VEC), q);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float u = p[i] * f[i].x - q[i] * f[i].y;
+            q[i] = q[i] * f[i].x + p[i] * f[i].y;
+            p[i] = u;
+          }
+          *reinterpret_cast<V*>(o + h * a.D + v * VEC) = rope_pack<VEC>(p);
+          *reinterpret_cast<V*>(o + h * a.D + half + v * VEC) = rope_pack<VEC>(q);
+        }
+      }
+    }
+  }
+}
+
+cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
+                        bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
+                        int64_t ldo, cudaStream_t st) {
+  RopeArgs a = {X, out, turns, pos, ldx, ldo, seq_len, (int)M, heads, D, rot, 1, 1, factor, transpose ? -1.f : 1.f};
+  a.tok = ROPE_TOK;
+  const unsigned grid = static_cast<unsigned>((M + a.tok - 1) / a.tok * a.hsplit);
+#define QL_ROPE(I_, V_) launch_pdl(rope_kernel<I_, V_>, dim3(grid), dim3(ROPE_THREADS), 0, st, a)
+  // the widest vector that divides the rotated part: heads start on 16 bytes (D % 8 == 0)
+  if (interleaved) {
+    if (rot % 8 == 0) return QL_ROPE(true, 8);
+    if (rot % 4 == 0) return QL_ROPE(true, 4);
+    return QL_ROPE(true, 2);
+  }
+  if (rot % 16 == 0) return QL_ROPE(false, 8);
+  if (rot % 8 == 0) return QL_ROPE(false, 4);
+  if (rot % 4 == 0) return QL_ROPE(false, 2);
+  return QL_ROPE(false, 1);
+#undef QL_ROPE
+}
+
+}  // namespace ql

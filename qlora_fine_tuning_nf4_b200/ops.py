@@ -12,6 +12,7 @@ touching memory out of range).
 """
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -42,6 +43,20 @@ class QloraLoraLinear(ctypes.Structure):
 class QloraLoraLinear16(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("n_out", ctypes.c_int64), ("k_in", ctypes.c_int64), ("A", ctypes.c_void_p),
                 ("B", ctypes.c_void_p), ("r", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class QloraFP8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_out", ctypes.c_int64), ("k_in", ctypes.c_int64)]
+
+
+class QloraFP8Rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class QloraLoraLinear8(ctypes.Structure):
+    _fields_ = [("w", QloraFP8), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("r", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class QloraMlpSaved(ctypes.Structure):
@@ -140,6 +155,35 @@ _SIGS = {
                                        ctypes.POINTER(QloraLoraLinear16), ctypes.POINTER(QloraLoraLinear16),
                                        ctypes.c_void_p, ctypes.POINTER(QloraMlpSaved), ctypes.c_void_p,
                                        ctypes.c_int64] + [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "fp8_quantize_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 3),
+    "fp8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 3),
+    "fp8_matmul_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 3),
+    "fp8_matmul": (ctypes.c_int, [ctypes.POINTER(QloraFP8Rows), ctypes.POINTER(QloraFP8), ctypes.c_int64,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "fp8_matmul_t": (ctypes.c_int, [ctypes.POINTER(QloraFP8Rows), ctypes.POINTER(QloraFP8), ctypes.c_int64,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_linear8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                        ctypes.c_int32]),
+    "qlora_linear8_fwd": (ctypes.c_int, [ctypes.POINTER(QloraLoraLinear8), ctypes.c_void_p,
+                                         ctypes.POINTER(QloraFP8Rows), ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_linear8_bwd": (ctypes.c_int, [ctypes.POINTER(QloraLoraLinear8), ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_add_rmsnorm_fwd": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int64, ctypes.c_int64, ctypes.c_float,
+                                                                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                                                     ctypes.POINTER(QloraFP8Rows), ctypes.c_void_p,
+                                                                     ctypes.c_void_p]),
+    "qlora_add_rmsnorm_bwd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_rope_fwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p]),
+    "qlora_rope_bwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p]),
 }
 
 
@@ -607,6 +651,355 @@ def qlora_qkv_bwd(q: LoraLinear, k: LoraLinear, v: LoraLinear, X, XA, dY, ws: Wo
     _check("qlora_qkv_bwd", lib().qlora_qkv_bwd(ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), _p(X), _p(XA),
                                                 _p(dY), M, *outs, _p(buf), buf.numel(), _stream()))
     return grads
+
+
+# ---------------------------------------------------------------- 8-bit ----
+
+FP8_BLOCK = 128  # columns of a row, or rows and columns of a weight, that share a scale
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+@dataclass
+class FP8Rows:
+    """Rows [M, K] in 8 bits: value = codes[m, k] * scale[k // 128, m]."""
+    codes: torch.Tensor  # float8_e4m3fn [M, K]
+    scale: torch.Tensor  # float32 [ceil(K / 128), M]
+
+    def c(self, name="rows", shape=None):
+        if not isinstance(self.codes, torch.Tensor) or self.codes.dim() != 2:
+            raise ValueError(f"{name}.codes must be a 2-D float8_e4m3fn tensor [M, K]")
+        M, K = shape or self.codes.shape
+        _t(self.codes, name + ".codes", (M, K), torch.float8_e4m3fn)
+        _t(self.scale, name + ".scale", (_blocks(K), M), torch.float32)
+        return QloraFP8Rows(self.codes.data_ptr(), self.scale.data_ptr())
+
+
+@dataclass
+class FP8Weight:
+    """Frozen weight [n_out, k_in] in 8 bits: value = codes[n, k] * scale[n // 128, k // 128]."""
+    codes: torch.Tensor  # float8_e4m3fn [n_out, k_in]
+    scale: torch.Tensor  # float32 [ceil(n_out / 128), ceil(k_in / 128)]
+
+    @property
+    def n_out(self):
+        return self.codes.shape[0]
+
+    @property
+    def k_in(self):
+        return self.codes.shape[1]
+
+    def c(self):
+        if not isinstance(self.codes, torch.Tensor) or self.codes.dim() != 2:
+            raise ValueError("codes must be a 2-D float8_e4m3fn tensor [n_out, k_in]")
+        _t(self.codes, "codes", tuple(self.codes.shape), torch.float8_e4m3fn)
+        _t(self.scale, "scale", (_blocks(self.n_out), _blocks(self.k_in)), torch.float32)
+        return QloraFP8(self.codes.data_ptr(), self.scale.data_ptr(), self.n_out, self.k_in)
+
+
+def _empty_rows(M, K, device):
+    return FP8Rows(torch.empty(M, K, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(_blocks(K), M, dtype=torch.float32, device=device))
+
+
+def fp8_quantize_rows(X, out: FP8Rows = None):
+    """bf16 rows [M, K] -> FP8Rows (one power-of-two scale per 128 columns)."""
+    M, K = _rows(X)
+    _t(X, "X", (M, K))
+    if out is None:
+        out = _empty_rows(M, K, X.device)
+    c = out.c("out", (M, K))
+    _check("fp8_quantize_rows", lib().fp8_quantize_rows(_p(X), M, K, c.codes, c.scale, _stream()))
+    return out
+
+
+def fp8_quantize(w):
+    """bf16 weight [n_out, k_in] on the GPU -> FP8Weight (one power-of-two scale per 128 x 128 block)."""
+    n_out, k_in = _rows(w, "w")
+    _t(w, "w", (n_out, k_in))
+    q = FP8Weight(torch.empty(n_out, k_in, dtype=torch.float8_e4m3fn, device=w.device),
+                  torch.empty(_blocks(n_out), _blocks(k_in), dtype=torch.float32, device=w.device))
+    _check("fp8_quantize", lib().fp8_quantize(_p(w), n_out, k_in, _p(q.codes), _p(q.scale), _stream()))
+    return q
+
+
+def fp8_matmul_workspace_bytes(M, K, N):
+    return int(lib().fp8_matmul_workspace_bytes(M, K, N))
+
+
+def _fp8_matmul(fn, x, w, ws, out, red, cols):
+    if not isinstance(x, FP8Rows) or not isinstance(w, FP8Weight):
+        raise TypeError(f"{fn} takes FP8Rows and FP8Weight")
+    cw = w.c()
+    if not isinstance(x.codes, torch.Tensor) or x.codes.dim() != 2:
+        raise ValueError("x.codes must be a 2-D float8_e4m3fn tensor")
+    M = x.codes.shape[0]
+    cx = x.c("x", (M, red(w)))
+    if out is None:
+        out = torch.empty(M, cols(w), dtype=torch.bfloat16, device=x.codes.device)
+    _t(out, "out", (M, cols(w)))
+    buf = ws.get(fp8_matmul_workspace_bytes(M, w.k_in, w.n_out))
+    _check(fn, getattr(lib(), fn)(ctypes.byref(cx), ctypes.byref(cw), M, _p(out), _p(buf), buf.numel(), _stream()))
+    return out
+
+
+def fp8_matmul(x: FP8Rows, w: FP8Weight, ws: Workspace, Y=None):
+    """Y = x W^T [M, n_out] in bf16 from x [M, k_in]."""
+    return _fp8_matmul("fp8_matmul", x, w, ws, Y, lambda w: w.k_in, lambda w: w.n_out)
+
+
+def fp8_matmul_t(dY: FP8Rows, w: FP8Weight, ws: Workspace, dX=None):
+    """dX = dY W [M, k_in] in bf16 from dY [M, n_out]."""
+    return _fp8_matmul("fp8_matmul_t", dY, w, ws, dX, lambda w: w.n_out, lambda w: w.k_in)
+
+
+@dataclass
+class LoraLinear8:
+    """A projection with a frozen e4m3 base weight."""
+    w: FP8Weight
+    A: torch.Tensor  # bf16 [k_in, r]
+    B: torch.Tensor  # bf16 [r, n_out]
+    scale: float
+
+    def c(self):
+        r = self.A.shape[1] if self.A.dim() == 2 else -1
+        cw = self.w.c()
+        _t(self.A, "A", (self.w.k_in, r))
+        _t(self.B, "B", (r, self.w.n_out))
+        return QloraLoraLinear8(cw, self.A.data_ptr(), self.B.data_ptr(), r, self.scale)
+
+
+def qlora_linear8_workspace_bytes(M, K, N, r=16):
+    return int(lib().qlora_linear8_workspace_bytes(M, K, N, r))
+
+
+def qlora_linear8_fwd(lin: LoraLinear8, X, ws: Workspace, Y=None, XA=None, X8: FP8Rows = None):
+    """Y = q(X) W^T + s (X A) B, XA = X A; X8 = X already in 8 bits (else the call quantises it)."""
+    M = _rows(X)[0]
+    c = lin.c()
+    n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
+    if Y is None:
+        Y = torch.empty(M, n_out, dtype=torch.bfloat16, device=X.device)
+    if XA is None:
+        XA = torch.empty(M, r, dtype=torch.bfloat16, device=X.device)
+    _t(X, "X", (M, k_in))
+    _t(Y, "Y", (M, n_out))
+    _t(XA, "XA", (M, r))
+    c8 = X8.c("X8", (M, k_in)) if X8 is not None else None
+    buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
+    _check("qlora_linear8_fwd", lib().qlora_linear8_fwd(ctypes.byref(c), _p(X), ctypes.byref(c8) if c8 else None, M,
+                                                        _p(Y), _p(XA), _p(buf), buf.numel(), _stream()))
+    return Y, XA
+
+
+def qlora_linear8_bwd(lin: LoraLinear8, X, XA, dY, ws: Workspace, dX=None, dA=None, dB=None):
+    M = _rows(X)[0]
+    c = lin.c()
+    n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
+    if dX is None:
+        dX = torch.empty(M, k_in, dtype=torch.bfloat16, device=X.device)
+    if dA is None:
+        dA = torch.empty_like(lin.A)
+    if dB is None:
+        dB = torch.empty_like(lin.B)
+    _t(X, "X", (M, k_in))
+    _t(XA, "XA", (M, r))
+    _t(dY, "dY", (M, n_out))
+    _t(dX, "dX", (M, k_in))
+    _t(dA, "dA", (k_in, r))
+    _t(dB, "dB", (r, n_out))
+    buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
+    _check("qlora_linear8_bwd", lib().qlora_linear8_bwd(ctypes.byref(c), _p(X), _p(XA), _p(dY), M, _p(dX), _p(dA),
+                                                        _p(dB), _p(buf), buf.numel(), _stream()))
+    return dX, dA, dB
+
+
+# -------------------------------------------------- residual add + norm ----
+
+def qlora_add_rmsnorm_fwd(X, R, w, eps, plus_one=False, H=None, Y=None, rstd=None, quantize=False, Y8: FP8Rows = None,
+                          want_y=True):
+    """H = X + R (R None: H is X), RMS norm of H with gain w (or 1 + w): returns (H, Y, rstd, Y8).
+
+    Y8 (FP8Rows of Y) is written with quantize=True or where it is given, else None; Y is None with
+    want_y=False.  H may be X or R."""
+    M, d = _rows(X)
+    _t(X, "X", (M, d))
+    if R is None:
+        if H is not None and H is not X:
+            raise ValueError("H is X itself where R is None")
+    else:
+        _t(R, "R", (M, d))
+        if H is None:
+            H = torch.empty_like(X)
+        _t(H, "H", (M, d))
+    if want_y and Y is None:
+        Y = torch.empty_like(X)
+    if Y is not None:
+        _t(Y, "Y", (M, d))
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=X.device)
+    if quantize and Y8 is None:
+        Y8 = _empty_rows(M, d, X.device)
+    _t(w, "w", (d,))
+    _t(rstd, "rstd", (M,), torch.float32)
+    c8 = Y8.c("Y8", (M, d)) if Y8 is not None else None
+    _check("qlora_add_rmsnorm_fwd", lib().qlora_add_rmsnorm_fwd(
+        _p(X), _p(R), _p(w), M, d, float(eps), int(bool(plus_one)), _p(None if R is None else H), _p(Y),
+        ctypes.byref(c8) if c8 else None, _p(rstd), _stream()))
+    return X if R is None else H, Y, rstd, Y8
+
+
+def qlora_add_rmsnorm_bwd(H, w, rstd, dY, dH=None, plus_one=False, dX=None):
+    """Gradient of X and of R: dH (what reaches H past the norm) plus the norm's.  dX may be dY or dH."""
+    M, d = _rows(H, "H")
+    if dX is None:
+        dX = torch.empty_like(H)
+    _t(H, "H", (M, d))
+    _t(w, "w", (d,))
+    _t(rstd, "rstd", (M,), torch.float32)
+    _t(dY, "dY", (M, d))
+    if dH is not None:
+        _t(dH, "dH", (M, d))
+    _t(dX, "dX", (M, d))
+    _check("qlora_add_rmsnorm_bwd", lib().qlora_add_rmsnorm_bwd(_p(H), _p(w), _p(rstd), _p(dY), _p(dH), M, d,
+                                                                int(bool(plus_one)), _p(dX), _stream()))
+    return dX
+
+
+# ----------------------------------------------------------------- rope ----
+
+@dataclass
+class RopePlan:
+    """Rotary frequencies of a model: pair i turns turns[i] / 2^64 of a circle per position."""
+    turns: torch.Tensor  # int64 [rot / 2], the bits of the 64-bit fractions
+    rot: int             # rotated elements of a head
+    factor: float        # cosines and sines are multiplied by it
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None):
+    """([radians per position of each pair], factor) in 64 bits.
+
+    base^(-2i / rot), changed by `scaling`, a dict whose "type" is
+      "linear"  frequencies / factor
+      "ntk"     base * factor^(rot / (rot - 2)): the slowest pair is stretched by factor, the fastest kept
+      "llama3"  pairs that turn less than low_freq_factor times in original_max_position are divided by
+                factor, those above high_freq_factor times kept, a linear blend between
+      "yarn"    pairs below beta_slow turns in original_max_position divided by factor, above beta_fast kept,
+                a linear ramp over the pair index between; cosines and sines times attention_factor
+                (0.1 ln(factor) + 1 unless given)."""
+    if not isinstance(rot, int) or rot <= 0 or rot % 2:
+        raise ValueError(f"rot must be a positive even integer, got {rot!r}")
+    base = float(base)
+    if not (base > 0.0 and math.isfinite(base)):
+        raise ValueError(f"base must be positive, got {base!r}")
+    s = dict(scaling or {"type": "none"})
+    kind = s.pop("type", None)
+    fields = {"none": (), "linear": ("factor",), "ntk": ("factor",),
+              "llama3": ("factor", "low_freq_factor", "high_freq_factor", "original_max_position"),
+              "yarn": ("factor", "original_max_position")}
+    if kind not in fields:
+        raise ValueError(f"unknown rope scaling {kind!r}: expected one of {sorted(fields)}")
+    optional = {"beta_fast": 32.0, "beta_slow": 1.0, "attention_factor": None} if kind == "yarn" else {}
+    missing, extra = set(fields[kind]) - set(s), set(s) - set(fields[kind]) - set(optional)
+    if missing or extra:
+        raise ValueError(f"rope scaling {kind!r}: missing {sorted(missing)}, not understood {sorted(extra)}")
+    f = float(s.get("factor", 1.0))
+    if not (f > 0.0 and math.isfinite(f)):
+        raise ValueError(f"rope scaling factor must be positive, got {f!r}")
+    if kind == "ntk":
+        if rot == 2:
+            raise ValueError("rope scaling 'ntk' needs more than one pair")
+        base *= f ** (rot / (rot - 2))
+    freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    factor = 1.0
+    if kind == "linear":
+        freq = [w / f for w in freq]
+    elif kind == "llama3":
+        lo, hi, n = float(s["low_freq_factor"]), float(s["high_freq_factor"]), float(s["original_max_position"])
+        if not (hi > lo):
+            raise ValueError("rope scaling 'llama3': high_freq_factor must be above low_freq_factor")
+        blend = [min(1.0, max(0.0, (n * w / (2 * math.pi) - lo) / (hi - lo))) for w in freq]
+        freq = [w * b + w / f * (1.0 - b) for w, b in zip(freq, blend)]
+    elif kind == "yarn":
+        n, opt = float(s["original_max_position"]), {**optional, **s}
+        if not (n > 0.0 and base > 1.0):
+            raise ValueError("rope scaling 'yarn' needs original_max_position > 0 and base > 1")
+        # the (real) pair index that turns `t` times in n positions: n base^(-2i / rot) = 2 pi t
+        index = lambda t: rot * math.log(n / (2 * math.pi * t)) / (2 * math.log(base))
+        lo = max(math.floor(index(float(opt["beta_fast"]))), 0)
+        hi = min(math.ceil(index(float(opt["beta_slow"]))), rot - 1)
+        ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(rot // 2)]
+        freq = [w / f * r + w * (1.0 - r) for w, r in zip(freq, ramp)]
+        a = opt["attention_factor"]
+        factor = (0.1 * math.log(f) + 1.0 if f > 1.0 else 1.0) if a is None else float(a)
+    return freq, factor
+
+
+def rope_plan(rot, base=10000.0, scaling=None, device="cuda"):
+    """RopePlan of `rope_frequencies(rot, base, scaling)` on the GPU; made once per model."""
+    freq, factor = rope_frequencies(rot, base, scaling)
+    bits = []
+    for w in freq:
+        t = int(round(w / (2 * math.pi) * 2.0 ** 64)) & (2 ** 64 - 1)
+        bits.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    return RopePlan(torch.tensor(bits, dtype=torch.int64, device=device), rot, factor)
+
+
+def _rope_rows(t, name, cols):
+    """Check of a bf16 [M, cols] operand whose rows may be a slice of wider ones; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} must have shape [M, {cols}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _rope(fn, X, heads, head_dim, plan, positions, seq_len, interleaved, out):
+    heads, head_dim = int(heads), int(head_dim)
+    cols = heads * head_dim
+    ldx = _rope_rows(X, "X", cols)
+    M = X.shape[0]
+    if out is None:
+        out = torch.empty(M, cols, dtype=torch.bfloat16, device=X.device)
+    ldo = _rope_rows(out, "out", cols)
+    if out.shape[0] != M:
+        raise ValueError(f"out must have {M} rows, got {out.shape[0]}")
+    if M > 0 and not (out.data_ptr() == X.data_ptr() and ldo == ldx):
+        # in place, apart in memory, or other columns of the same rows
+        a, b = X.data_ptr() // 2, out.data_ptr() // 2
+        if a < b + (M - 1) * ldo + cols and b < a + (M - 1) * ldx + cols:
+            if ldx != ldo or not cols <= (b - a) % ldx <= ldx - cols:
+                raise ValueError("out overlaps X without being X")
+    _t(plan.turns, "plan.turns", (plan.rot // 2,), torch.int64)
+    if positions is not None:
+        if seq_len:
+            raise ValueError("give positions or seq_len, not both")
+        _t(positions, "positions", (M,), torch.int64)
+    _check(fn, getattr(lib(), fn)(_p(X), M, ldx, heads, head_dim, _p(plan.turns), plan.rot, int(bool(interleaved)),
+                                  plan.factor, _p(positions), int(seq_len), _p(out), ldo, _stream()))
+    return out
+
+
+def qlora_rope_fwd(X, heads, head_dim, plan: RopePlan, positions=None, seq_len=0, interleaved=False, out=None):
+    """Rotary positions on X [M, heads * head_dim], whose rows may be a slice of wider ones (the q and k
+    columns of qlora_qkv_fwd's Y).  Row m has positions[m] (int64), else m % seq_len (m if 0).  out=X rotates
+    in place."""
+    return _rope("qlora_rope_fwd", X, heads, head_dim, plan, positions, seq_len, interleaved, out)
+
+
+def qlora_rope_bwd(dY, heads, head_dim, plan: RopePlan, positions=None, seq_len=0, interleaved=False, out=None):
+    """The gradient of qlora_rope_fwd's X: the transposed rotation of dY."""
+    return _rope("qlora_rope_bwd", dY, heads, head_dim, plan, positions, seq_len, interleaved, out)
 
 
 # ------------------------------------------------------------ utilities ----
