@@ -12,12 +12,31 @@
 //
 // Structure (persistent; one 256 x 256 output tile at a time per CTA pair):
 //   warp 0       TMA producer: A and W tiles (128 x 128 bytes each), LoRA operands
-//   warp 1       TMEM allocation; lane 0 of the leader CTA issues tcgen05.mma
-//   warps 2-9    accumulate: TMEM -> scale -> registers; at the tile's end
+//   warp 1       TMEM allocation; the leader CTA's issues tcgen05.mma
+//   warp 2       scales: sa * sw of a block's rows and two column blocks into a
+//                shared-memory ring, ahead of the MMA
+//   warps 4-11   accumulate: TMEM -> scale -> registers; at the tile's end
 //                registers -> bf16 -> shared memory -> TMA store
 // Two TMEM accumulators of 256 columns alternate per reduction block, so the MMA
 // of one block runs while the previous one is being added.  The LoRA term is one
 // more block: bf16 operands (kind::f16) and scale 1.
+//
+// What bounds it.  Per block and SM the tensor core needs 512 cycles, 32 KB come
+// from L2 (64 bytes a cycle: 512 as well), and the accumulating warps 256 cycles
+// of fma and as many of TMEM loads per scheduler.  8192 x 4096 x 11008 takes 0.31
+// ms (2.36 PFLOP/s); the same kernel without the scaling, adding the blocks in
+// TMEM, 0.24 ms.  On the way there, each measured on that product:
+//  * issuing from one elected thread of a converged warp (elect.sync) instead of
+//    under `lane == 0`: 0.39 -> 0.35 ms.  Under a divergent branch every MMA,
+//    commit and TMA load costs tens of cycles more, and the issue loop is one
+//    serial chain that every block passes through;
+//  * scales through shared memory from a warp of their own: 0.35 -> 0.31 ms.
+//    Loaded by the accumulating warps themselves, even four blocks ahead, they
+//    make those warps wait for an L2 round trip along with their TMEM loads;
+//  * 160 columns with three accumulators, or two accumulators of 192: fewer
+//    stalls between accumulators, but 15-30% more bytes from L2 per product:
+//    0.38 ms;
+//  * sixteen accumulating warps, or packed pairs of fma: no gain.
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -26,22 +45,35 @@ namespace ql {
 struct Gemm8Cfg {
   static constexpr int BM = 128;    // rows per CTA
   static constexpr int BNT = 256;   // columns per tile
-  static constexpr int BNC = 128;   // columns of W each CTA of the pair loads
+  static constexpr int BNC = 128;   // columns of W each CTA of the pair loads; columns per accumulating warp
   static constexpr int BK = 128;    // reduction block: one scale, one 128-byte row
   static constexpr int TILE = BM * BK;  // bytes of an A or W tile
   static constexpr int S = 6;       // operand stages
+  // Scale slots.  A slot is written once its block's operand stage is free, at most S blocks ahead of
+  // the MMA, which is at most two ahead of the accumulating warps, which read a block's scale before
+  // they release its accumulator: S + 4 slots need no barrier of their own.
+  static constexpr int SR = S + 4;
+  static constexpr int SC_FLOATS = 2 * BM;  // [column half][row]
+  static constexpr int G = 4;       // blocks whose scales are requested together
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARP0 = 4;  // warp 3 fills the first warp group
+  static constexpr int EPI_SLOT = 32 * 32 * 2;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + S * TILE;
   static constexpr int OFF_EPI = OFF_B + S * TILE;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int EPI_WARP0 = 2;
-  static constexpr int EPI_SLOT = 32 * 32 * 2;
-  static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_SLOT;
+  static constexpr int OFF_SC = OFF_EPI + EPI_WARPS * EPI_SLOT;
+  static constexpr int OFF_BAR = OFF_SC + SR * SC_FLOATS * 4;
   static constexpr int NBAR = 2 * S + 5;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int TMEM_COLS = 512;
+  // The accumulating warps hold 128 sums and two 32-register TMEM loads each: more than the 168
+  // registers a thread that 384 threads leave.  Warp group 0 gives up what it does not need:
+  // 40 + 2 * 232 = 3 * 168.
+  static constexpr int REGS_PRODUCER = 40, REGS_EPI = 232, REGS_LAUNCH = 168;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(THREADS == 384 && REGS_PRODUCER + 2 * REGS_EPI == 3 * REGS_LAUNCH && REGS_LAUNCH * THREADS <= 65536,
+                "the warp groups' registers add up to the launch's");
 };
 
 template <bool BWD>
@@ -51,7 +83,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
 
@@ -74,11 +106,12 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   const uint32_t acc_full0 = bar0 + 8u * (2 * C::S);
   const uint32_t acc_empty0 = acc_full0 + 16u;
   const uint32_t drain_bar = acc_full0 + 32u;
+  float* const scales = reinterpret_cast<float*>(sgen + C::OFF_SC);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sgen + C::OFF_BAR + C::NBAR * 8);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), 3);  // the loads, and each CTA's scales
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -96,6 +129,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+  const uint32_t lead0 = mapa_shared(bar0, 0);  // the leader CTA's barriers
   grid_dep_wait();
   grid_dep_launch();
 
@@ -109,127 +143,177 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
     n0 = (r / gm) * C::BNT;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
+  if (warp < C::EPI_WARP0) {
+    setmaxnreg_dec<C::REGS_PRODUCER>();
+    if (warp == 0) {
+      // ---------------------------------------------------- TMA producer --
       bool ok = true;
-      tma_prefetch_desc(&maps.a);
-      tma_prefetch_desc(&maps.b);
-      int j = 0;
+      int s = 0;
+      uint32_t ph = 1;
       for (int t = cluster; t < total_tiles && ok; t += clusters) {
         int m0, n0;
         tile_coords(t, m0, n0);
         const int col = n0 + static_cast<int>(rank) * C::BNC;  // this CTA's share of the tile's columns
-        for (int kb = 0; kb < blocks; ++kb, ++j) {
-          const int s = j % C::S;
-          ok = mbar_wait(empty_bar(s), ((j / C::S) & 1) ^ 1, args.status);
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, args.status));
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 4 * C::TILE);
-          const uint32_t bar = mapa_shared(full_bar(s), 0);  // both CTAs' loads complete on the leader's barrier
-          const uint32_t a = sbase + C::OFF_A + s * C::TILE, b = sbase + C::OFF_B + s * C::TILE;
-          if (kb < args.nkb) {
-            tma_load_2d_pair(a, &maps.a, bar, kb * C::BK, m0);
-            // W rows x reduction bytes (K-major), or reduction rows x output columns (MN-major)
-            if (BWD) tma_load_2d_pair(b, &maps.b, bar, col, kb * C::BK);
-            else tma_load_2d_pair(b, &maps.b, bar, kb * C::BK, col);
-          } else {
-            // LoRA operands, 64 wide with zeros beyond the rank
-            tma_load_2d_pair(a, &maps.la, bar, 0, m0);
-            if (BWD) {
-              tma_load_2d_pair(b, &maps.lb, bar, 0, col);
+          if (elect_one()) {
+            // both CTAs' loads complete on the leader's barrier
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 4 * C::TILE);
+            const uint32_t bar = lead0 + 8u * s;
+            const uint32_t a = sbase + C::OFF_A + s * C::TILE, b = sbase + C::OFF_B + s * C::TILE;
+            if (kb < args.nkb) {
+              tma_load_2d_pair(a, &maps.a, bar, kb * C::BK, m0);
+              // W rows x reduction bytes (K-major), or reduction rows x output columns (MN-major)
+              if (BWD) tma_load_2d_pair(b, &maps.b, bar, col, kb * C::BK);
+              else tma_load_2d_pair(b, &maps.b, bar, kb * C::BK, col);
             } else {
-              tma_load_2d_pair(b, &maps.lb, bar, col, 0);
-              tma_load_2d_pair(b + 8192, &maps.lb, bar, col + 64, 0);
+              // LoRA operands, 64 wide with zeros beyond the rank: A [128 columns, r] K-major (dX), or
+              // B [r, 128 columns] MN-major in chunks of 64 columns (forward)
+              tma_load_2d_pair(a, &maps.la, bar, 0, m0);
+              if (BWD) {
+                tma_load_2d_pair(b, &maps.lb, bar, 0, col);
+              } else {
+                tma_load_2d_pair(b, &maps.lb, bar, col, 0);
+                tma_load_2d_pair(b + 8192, &maps.lb, bar, col + 64, 0);
+              }
             }
           }
+          __syncwarp();
+          if (++s == C::S) s = 0, ph ^= 1;
         }
       }
-      if (!ok) settle_inflight();
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------- MMA -----
-    if (rank == 0 && lane == 0) {
+      if (!ok) settle_inflight();  // loads already issued land before the CTA can exit
+    } else if (warp == 1 && rank == 0) {
+      // --------------------------------------------------------- MMA -----
+      // Descriptors and phases are carried along: this loop is one serial chain.
       bool ok = true;
       constexpr uint32_t idesc = idesc_e4m3(2 * C::BM, C::BNT, false, BWD);
       constexpr uint32_t idesc_lora = idesc_bf16(2 * C::BM, C::BNT, false, !BWD);
-      int j = 0;
+      const uint64_t ad0 = smem_desc(sbase + C::OFF_A, 16, 1024, QL_SWZ_128B);
+      const uint64_t bd0 = smem_desc(sbase + C::OFF_B, BWD ? C::TILE : 16, 1024, QL_SWZ_128B);
+      const uint64_t bl0 = smem_desc(sbase + C::OFF_B, BWD ? 16 : 8192, 1024, QL_SWZ_128B);
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 1;  // phases of the operand ring and of the accumulators
       for (int t = cluster; t < total_tiles && ok; t += clusters) {
-        for (int kb = 0; kb < blocks; ++kb, ++j) {
-          const int s = j % C::S, b = j & 1;
-          ok = mbar_wait(acc_empty0 + 8u * b, ((j >> 1) & 1) ^ 1, args.status) &&
-               mbar_wait(full_bar(s), (j / C::S) & 1, args.status);
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = mbar_wait(full_bar(s), ph, args.status) && mbar_wait(acc_empty0 + 8u * b, aph, args.status);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t acc = tmem + b * C::BNT;
-          const uint32_t as = sbase + C::OFF_A + s * C::TILE, bs = sbase + C::OFF_B + s * C::TILE;
-          if (kb < args.nkb) {
+          if (elect_one()) {
+            const uint32_t acc = tmem + b * C::BNT;
+            const uint64_t so = static_cast<uint64_t>(s) * (C::TILE >> 4);
+            if (kb < args.nkb) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {  // 32 reduction elements each
-              const uint64_t ad = smem_desc(as + kk * 32, 16, 1024, QL_SWZ_128B);
-              const uint64_t bd = BWD ? smem_desc(bs + kk * 4096, C::TILE, 1024, QL_SWZ_128B)
-                                      : smem_desc(bs + kk * 32, 16, 1024, QL_SWZ_128B);
-              umma_e4m3<2>(acc, ad, bd, idesc, kk != 0);
+              for (int kk = 0; kk < 4; ++kk)  // 32 reduction elements each
+                umma_e4m3<2>(acc, ad0 + so + kk * 2, bd0 + so + kk * (BWD ? 256 : 2), idesc, kk != 0);
+            } else {
+              for (int kk = 0; kk < args.lora_k16; ++kk)
+                umma_bf16<2>(acc, ad0 + so + kk * 2, bl0 + so + kk * (BWD ? 2 : 128), idesc_lora, kk != 0);
             }
-          } else {
-            for (int kk = 0; kk < args.lora_k16; ++kk) {
-              const uint64_t ad = smem_desc(as + kk * 32, 16, 1024, QL_SWZ_128B);
-              const uint64_t bd = BWD ? smem_desc(bs + kk * 32, 16, 1024, QL_SWZ_128B)
-                                      : smem_desc(bs + kk * 2048, 8192, 1024, QL_SWZ_128B);
-              umma_bf16<2>(acc, ad, bd, idesc_lora, kk != 0);
-            }
+            umma_commit<2>(empty_bar(s));
+            umma_commit<2>(acc_full0 + 8u * b);
           }
-          umma_commit<2>(empty_bar(s));
-          umma_commit<2>(acc_full0 + 8u * b);
+          __syncwarp();
+          if (++s == C::S) s = 0, ph ^= 1;
+          aph ^= b;
+          b ^= 1;
         }
       }
       // let every issued MMA finish before TMEM can be released (after an error too)
-      umma_commit<2>(drain_bar);
+      if (elect_one()) umma_commit<2>(drain_bar);
+      __syncwarp();
       mbar_drain(drain_bar, 0);
+    } else if (warp == 2) {
+      // ------------------------------------------------------ scales -----
+      // G blocks' scales are requested at once and written as their operand stages come free.  The
+      // arrival on the stage's full barrier orders them before the block's MMA, and so before its
+      // accumulator is handed over.  Rows past the last one add zeros: any scale will do.
+      bool ok = true;
+      int s = 0, sl = 0;
+      uint32_t ph = 1;
+      for (int t = cluster; t < total_tiles && ok; t += clusters) {
+        int m0, n0;
+        tile_coords(t, m0, n0);
+        const int nb = min(n0 / 128 + (lane & 1), (args.N - 1) / 128);
+        const float* sb = args.sb + static_cast<size_t>(nb) * args.sb_n;
+        for (int kb = 0; kb < blocks && ok; kb += C::G) {
+          float va[C::G][4];
+#pragma unroll
+          for (int g = 0; g < C::G; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = m0 + i * 32 + lane;
+              va[g][i] = kb + g < args.nkb && row < args.M
+                             ? __ldg(args.sa + static_cast<size_t>(kb + g) * args.M + row)
+                             : 1.f;
+            }
+          const int kw = kb + (lane >> 1);
+          const float vb = lane < 2 * C::G && kw < args.nkb ? __ldg(sb + static_cast<size_t>(kw) * args.sb_k) : 1.f;
+#pragma unroll
+          for (int g = 0; g < C::G; ++g) {
+            if (kb + g >= blocks) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, args.status));
+            if (!ok) break;
+            const float w0 = __shfl_sync(0xffffffffu, vb, 2 * g), w1 = __shfl_sync(0xffffffffu, vb, 2 * g + 1);
+            float* d = scales + sl * C::SC_FLOATS + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              d[i * 32] = va[g][i] * w0;
+              d[C::BM + i * 32] = va[g][i] * w1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead0 + 8u * s);
+            if (++s == C::S) s = 0, ph ^= 1;
+            if (++sl == C::SR) sl = 0;
+          }
+        }
+      }
     }
   } else {
     // ------------------------------------------------------ accumulate ---
+    setmaxnreg_inc<C::REGS_EPI>();
     const int ew = warp - C::EPI_WARP0;
     const int lg = warp & 3;    // TMEM lane quadrant this warp may access
     const int half = ew >> 2;   // its 128 columns of the tile: one weight scale per reduction block
     const uint32_t stg = sbase + C::OFF_EPI + ew * C::EPI_SLOT;
     uint8_t* stg_g = sgen + C::OFF_EPI + ew * C::EPI_SLOT;
     const uint64_t pol = l2_policy_evict_first();
-    int j = 0;
+    const float* my_scale = scales + half * C::BM + lg * 32 + lane;
+    int b = 0, sl = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (int t = cluster; t < total_tiles && ok; t += clusters) {
       int m0, n0;
       tile_coords(t, m0, n0);
-      const int row = m0 + lg * 32 + lane;
-      const int nb = n0 / 128 + half;
-      const bool in = row < args.M && nb * 128 < args.N;
-      const float* sa = args.sa + row;
-      const float* sb = args.sb + static_cast<size_t>(nb) * args.sb_n;
-      auto scale_of = [&](int kb) {
-        if (kb >= args.nkb) return 1.f;
-        return in ? __ldg(sa + static_cast<size_t>(kb) * args.M) * __ldg(sb + static_cast<size_t>(kb) * args.sb_k) : 0.f;
-      };
-      float acc[128];
+      float acc[C::BNC];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      float next = scale_of(0);
-      for (int kb = 0; kb < blocks; ++kb, ++j) {
-        const int b = j & 1;
-        const float sc = next;
-        if (kb + 1 < blocks) next = scale_of(kb + 1);
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full0 + 8u * b, (j >> 1) & 1, args.status));
+      for (int i = 0; i < C::BNC; ++i) acc[i] = 0.f;
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full0 + 8u * b, ph, args.status));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t tacc = tmem + b * C::BNT + half * 128 + (static_cast<uint32_t>(lg * 32) << 16);
+        const float sc = my_scale[sl * C::SC_FLOATS];
+        if (++sl == C::SR) sl = 0;
+        const uint32_t tacc = tmem + b * C::BNT + half * C::BNC + (static_cast<uint32_t>(lg * 32) << 16);
+        uint32_t v[2][32];  // 32 columns are loaded while the previous 32 are added
+        tmem_ld_32x32b_x32_async(tacc, v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld_32x32b_x32(tacc + c * 32, v);
+          tmem_wait_ld(v[c & 1]);
+          if (c < 3) {
+            tmem_ld_32x32b_x32_async(tacc + (c + 1) * 32, v[(c + 1) & 1]);
+          } else {  // every value is in registers: the MMA may have the accumulator back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead0 + (acc_empty0 - bar0) + 8u * b);
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], sc, acc[c * 32 + i]);
+          for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(v[c & 1][i]), sc, acc[c * 32 + i]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_empty0 + 8u * b, 0));
+        ph ^= b;
+        b ^= 1;
       }
       if (!ok) break;
       // 32 x 32 chunks through this warp's shared slot (64B swizzle); the TMA store clips at the edges
@@ -247,7 +331,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&maps.out, stg, n0 + half * 128 + c * 32, m0 + lg * 32, pol);
+          tma_store_2d(&maps.out, stg, n0 + half * C::BNC + c * 32, m0 + lg * 32, pol);
           bulk_commit_group();
         }
       }
