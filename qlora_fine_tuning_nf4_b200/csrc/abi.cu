@@ -45,7 +45,12 @@ cudaError_t launch_add_rmsnorm_bwd(const bf16* H, const bf16* w, const float* rs
 cudaError_t launch_fp8_quantize_rows(const bf16* X, int64_t M, int64_t K, uint8_t* codes, float* scale,
                                      cudaStream_t st);
 cudaError_t launch_fp8_quantize(const bf16* w, int64_t N, int64_t K, uint8_t* codes, float* scale, cudaStream_t st);
-cudaError_t launch_gemm_fp8(bool bwd, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
+cudaError_t launch_gemm_fp8(bool bwd, int bn, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
+cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
+                                cudaStream_t st);
+cudaError_t launch_gemm_fp8_few(bool bwd, const uint8_t* x, const float* sa, const uint8_t* w, const float* sb,
+                                int sb_k, int sb_n, int M, int red, int cols, int ldw, const bf16* L, const bf16* R,
+                                int r, bf16* out, cudaStream_t st);
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
                         int64_t ldo, cudaStream_t st);
@@ -61,12 +66,13 @@ namespace {
 enum KernelId : int {
   K_QUANT = 0, K_DEQUANT, K_GEMM_FWD, K_GEMM_GLU_FWD, K_GEMM_BWD, K_GEMM_GLU_BWD, K_ROWPROJ, K_COLPROJ, K_DYPASS,
   K_REDUCE, K_NORM_FWD, K_NORM_BWD, K_ADDNORM_FWD, K_ADDNORM_BWD, K_FP8_ROWS, K_FP8_QUANT, K_GEMM8_FWD, K_GEMM8_BWD,
-  K_ROPE, K_COUNT
+  K_GEMM8_SUM, K_ROPE, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "gemm_nf4_fwd", "gemm_nf4_gateup_glu_fwd", "gemm_nf4_bwd_dx",
     "gemm_nf4_down_bwd_glu", "skinny_rowproj", "skinny_colproj", "skinny_dypass", "skinny_reduce", "rmsnorm_fwd", "rmsnorm_bwd",
-    "add_rmsnorm_fwd", "add_rmsnorm_bwd", "fp8_quantize_rows", "fp8_quantize", "gemm_fp8_fwd", "gemm_fp8_bwd_dx", "rope"};
+    "add_rmsnorm_fwd", "add_rmsnorm_bwd", "fp8_quantize_rows", "fp8_quantize", "gemm_fp8_fwd", "gemm_fp8_bwd_dx",
+    "gemm_fp8_sum", "rope"};
 
 std::atomic<uint64_t> g_launches{0};
 bool g_trace = false;
@@ -1435,21 +1441,63 @@ qlora_status check_fp8(const qlora_fp8* w) {
   if (misaligned(w->codes) || misaligned(w->scale)) return QLORA_ERR_MISALIGNED;
   return QLORA_OK;
 }
+// How a product of M rows, `red` reduction elements and `out` columns is run.
+struct Fp8Plan {
+  bool few;    // warp-level MMAs that stream the weight (gemm_fp8_few.cu)
+  int bn;      // columns per tile of the tcgen05 kernel
+  int splits;  // parts of its reduction
+};
+// Measured (us, one product; 4096 -> 4096 unless said otherwise):
+//  * few rows or tcgen05: 16 rows 5.7 vs 12.1; 32 rows 8.7 vs 11.4, but 28.4 vs 16.5 for 14336
+//    columns (more CTAs than SMs) and 32.9 vs 22.2 for a reduction of 14336 (long chains per warp);
+//  * 128 or 256 columns per tile: 256 rows 12.4 vs 15.8 (32 or 16 tiles on 74 CTA pairs), 1024 rows
+//    22.2 vs 17.7;
+//  * parts of the reduction, where the tiles leave half the pairs idle: 256 rows, 14336 -> 4096 24.0 vs
+//    33.9; 128 rows, 4096 -> 1024 8.9 vs 12.2.  A part shorter than six blocks does not pay for the
+//    launch that adds the parts.
+Fp8Plan plan_fp8(int64_t M, int64_t red, int64_t out) {
+  const int64_t sms = num_sms(), pairs = sms / 2, mt = cdiv(M, 256), nkb = cdiv(red, 128);
+  Fp8Plan p = {M <= 16 || (M <= 32 && cdiv(out, 32) <= sms && nkb <= 48), 256, 1};
+  if (p.few) return p;
+  if (mt * cdiv(out, 256) * 2 <= pairs) p.bn = 128;
+  const int64_t tiles = mt * cdiv(out, p.bn);
+  if (tiles * 2 <= pairs) p.splits = (int)std::max<int64_t>(1, std::min(pairs / tiles, nkb / 6));
+  return p;
+}
+// fp32 partials of a split reduction
+size_t fp8_part_bytes(int64_t M, int64_t red, int64_t out) {
+  const Fp8Plan p = plan_fp8(M, red, out);
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * cdiv(M, 256) * 256 * out * 4 : 0;
+}
 // D = x W^T (bwd = false) or x W, plus L Rt with the LoRA operands L [M, r] and B [r, n_out] or
-// A [k_in, r] (r = 0: none).
+// A [k_in, r] (r = 0: none).  `part` has room for fp8_part_bytes.
 qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const qlora_fp8& w, int64_t M, bf16* D,
-                      const bf16* L, const bf16* Rf, int r, int* status, cudaStream_t st) {
+                      const bf16* L, const bf16* Rf, int r, float* part, int* status, cudaStream_t st) {
   const int64_t K = w.k_in, N = w.n_out;
   const int64_t red = bwd ? N : K, out = bwd ? K : N;
+  const int wkb = (int)cdiv(K, 128);  // the weight's scales are [ceil(n_out / 128), ceil(k_in / 128)]
+  const int sb_k = bwd ? wkb : 1, sb_n = bwd ? 1 : wkb;
+  const Fp8Plan plan = plan_fp8(M, red, out);
+  if (plan.few) {
+    KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
+    return cuda_status(launch_gemm_fp8_few(bwd, codes, scale, w.codes, w.scale, sb_k, sb_n, (int)M, (int)red, (int)out,
+                                           (int)K, L, Rf, r, D, st));
+  }
+  const int bn = plan.bn;
+  const int64_t prows = cdiv(M, 256) * 256;
   Gemm8Maps maps;
   std::memset(&maps, 0, sizeof(maps));
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!make_map(&maps.a, u8, 1, codes, red, M, red, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&maps.b, u8, 1, w.codes, K, N, K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.b, u8, 1, w.codes, K, N, K, bwd ? bn / 2 : 128, bwd ? 128 : bn / 2,
+                bwd && bn == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
       !map_bf16(&maps.out, D, out, M, out, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return QLORA_ERR_CUDA;
+  if (plan.splits > 1 && !make_map(&maps.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, out, prows * plan.splits, out,
+                                   32, 16, CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
   if (r > 0 && (!map_bf16(&maps.la, L, r, M, r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-                !(bwd ? map_bf16(&maps.lb, Rf, r, K, r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)
+                !(bwd ? map_bf16(&maps.lb, Rf, r, K, r, 64, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B)
                       : map_bf16(&maps.lb, Rf, N, r, N, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))))
     return QLORA_ERR_CUDA;
   Gemm8Args a;
@@ -1460,13 +1508,19 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
   a.lora_k16 = r / 16;
   a.sa = scale;
   a.sb = w.scale;
-  const int wkb = (int)cdiv(K, 128);  // the weight's scales are [ceil(n_out / 128), ceil(k_in / 128)]
-  a.sb_k = bwd ? wkb : 1;
-  a.sb_n = bwd ? 1 : wkb;
+  a.sb_k = sb_k;
+  a.sb_n = sb_n;
   a.status = status;
   a.group_m = kGroupM;
-  KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
-  return cuda_status(launch_gemm_fp8(bwd, maps, a, st));
+  a.splits = plan.splits;
+  a.prows = (int)prows;
+  {
+    KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
+    const qlora_status s = cuda_status(launch_gemm_fp8(bwd, bn, maps, a, st));
+    if (s != QLORA_OK || plan.splits == 1) return s;
+  }
+  KScope k(K_GEMM8_SUM, st);
+  return cuda_status(launch_gemm_fp8_sum(part, prows, plan.splits, M, out, D, st));
 }
 
 qlora_status fp8_matmul_any(bool bwd, const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* out,
@@ -1480,13 +1534,14 @@ qlora_status fp8_matmul_any(bool bwd, const qlora_fp8_rows* x, const qlora_fp8* 
   if (M > kMaxDim) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < fp8_matmul_workspace_bytes(M, w->k_in, w->n_out)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   return gemm_fp8(bwd, x->codes, x->scale, *w, M, reinterpret_cast<bf16*>(out), nullptr, nullptr, 0,
-                  static_cast<int*>(ws), reinterpret_cast<cudaStream_t>(stream));
+                  reinterpret_cast<float*>(static_cast<char*>(ws) + 256), static_cast<int*>(ws),
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
 size_t fp8_matmul_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out) {
-  (void)M, (void)k_in, (void)n_out;
-  return 256;
+  if (M <= 0 || k_in <= 0 || n_out <= 0) return 256;
+  return 256 + std::max(fp8_part_bytes(M, k_in, n_out), fp8_part_bytes(M, n_out, k_in));
 }
 qlora_status fp8_matmul(const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* Y, void* ws,
                         size_t ws_bytes, qlora_stream_t stream) {
@@ -1512,6 +1567,7 @@ Linear8Ws linear8_ws(int64_t M, int64_t K, int64_t N, int r) {
   size_t part = rowproj_part_bytes(M, K, r);
   part = std::max(part, dypass_part_bytes(M, N, r));
   part = std::max(part, colproj_part_bytes(M, K, r));
+  part = std::max(part, std::max(fp8_part_bytes(M, K, N), fp8_part_bytes(M, N, K)));
   w.total = w.part + align256(part);
   return w;
 }
@@ -1562,7 +1618,7 @@ qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* 
                    routs(rout(xa, 0, r, r, 0, 1.f), rout(scaled ? XAs : nullptr, 0, r, r, 0, lin->scale)), status, st);
   if (s != QLORA_OK) return s;
   return gemm_fp8(false, codes, scale, lin->w, M, reinterpret_cast<bf16*>(Y), XAs,
-                  reinterpret_cast<const bf16*>(lin->B), r, status, st);
+                  reinterpret_cast<const bf16*>(lin->B), r, reinterpret_cast<float*>(w + l.part), status, st);
 }
 
 qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* X, const qlora_bf16* XA_saved,
@@ -1600,7 +1656,7 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
                   routs(rout(reinterpret_cast<bf16*>(dB), 0, r, (int)N, 1, sc)), status, st);
   if (s != QLORA_OK) return s;
   s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG, reinterpret_cast<const bf16*>(lin->A),
-               r, status, st);
+               r, part, status, st);
   if (s != QLORA_OK) return s;
   return pass_colproj(reinterpret_cast<const bf16*>(X), M, K, sG, r, part,
                       routs(rout(reinterpret_cast<bf16*>(dA), 0, r, r, 0, 1.f)), status, st);

@@ -42,44 +42,50 @@
 
 namespace ql {
 
+// BN: output columns per tile, 256 or 128.
+template <int BN>
 struct Gemm8Cfg {
   static constexpr int BM = 128;    // rows per CTA
-  static constexpr int BNT = 256;   // columns per tile
-  static constexpr int BNC = 128;   // columns of W each CTA of the pair loads; columns per accumulating warp
+  static constexpr int BNT = BN;
+  static constexpr int BNC = BN / 2;  // columns of W each CTA of the pair loads; columns per accumulating warp
   static constexpr int BK = 128;    // reduction block: one scale, one 128-byte row
-  static constexpr int TILE = BM * BK;  // bytes of an A or W tile
-  static constexpr int S = 6;       // operand stages
+  static constexpr int ACCS = 512 / BN;  // TMEM accumulators
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int B_BYTES = BNC * BK;
+  static constexpr int S = BN == 256 ? 6 : 8;  // operand stages
   // Scale slots.  A slot is written once its block's operand stage is free, at most S blocks ahead of
-  // the MMA, which is at most two ahead of the accumulating warps, which read a block's scale before
-  // they release its accumulator: S + 4 slots need no barrier of their own.
-  static constexpr int SR = S + 4;
-  static constexpr int SC_FLOATS = 2 * BM;  // [column half][row]
+  // the MMA, which is at most ACCS ahead of the accumulating warps, which read a block's scale before
+  // they release its accumulator: S + ACCS + 2 slots need no barrier of their own.
+  static constexpr int SR = S + ACCS + 2;
+  static constexpr int NBLK = BN / 128;     // weight blocks side by side in a tile
+  static constexpr int SC_FLOATS = NBLK * BM;  // [weight block][row]
   static constexpr int G = 4;       // blocks whose scales are requested together
   static constexpr int EPI_WARPS = 8;
   static constexpr int EPI_WARP0 = 4;  // warp 3 fills the first warp group
   static constexpr int EPI_SLOT = 32 * 32 * 2;
   static constexpr int OFF_A = 0;
-  static constexpr int OFF_B = OFF_A + S * TILE;
-  static constexpr int OFF_EPI = OFF_B + S * TILE;
+  static constexpr int OFF_B = OFF_A + S * A_BYTES;
+  static constexpr int OFF_EPI = OFF_B + S * B_BYTES;
   static constexpr int OFF_SC = OFF_EPI + EPI_WARPS * EPI_SLOT;
   static constexpr int OFF_BAR = OFF_SC + SR * SC_FLOATS * 4;
-  static constexpr int NBAR = 2 * S + 5;
+  static constexpr int NBAR = 2 * S + 2 * ACCS + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int TMEM_COLS = 512;
-  // The accumulating warps hold 128 sums and two 32-register TMEM loads each: more than the 168
+  // The accumulating warps hold up to 128 sums and two 32-register TMEM loads each: more than the 168
   // registers a thread that 384 threads leave.  Warp group 0 gives up what it does not need:
   // 40 + 2 * 232 = 3 * 168.
   static constexpr int REGS_PRODUCER = 40, REGS_EPI = 232, REGS_LAUNCH = 168;
+  static_assert(BN == 256 || BN == 128, "tile width");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(THREADS == 384 && REGS_PRODUCER + 2 * REGS_EPI == 3 * REGS_LAUNCH && REGS_LAUNCH * THREADS <= 65536,
                 "the warp groups' registers add up to the launch's");
 };
 
-template <bool BWD>
-__global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
+template <bool BWD, int BN>
+__global__ void __launch_bounds__(Gemm8Cfg<BN>::THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ Gemm8Maps maps, const Gemm8Args args) {
-  using C = Gemm8Cfg;
+  using C = Gemm8Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -89,12 +95,12 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
 
   const int n_tiles = (args.N + C::BNT - 1) / C::BNT;
   const int m_tiles = (args.M + 2 * C::BM - 1) / (2 * C::BM);
-  const int total_tiles = n_tiles * m_tiles;
+  // units of work: a tile, or one of `splits` parts of a tile's reduction
+  const int units = n_tiles * m_tiles * args.splits;
   const int cluster = blockIdx.x / 2;
   const int clusters = gridDim.x / 2;
-  const int blocks = args.nkb + (args.lora_k16 > 0 ? 1 : 0);  // accumulator blocks per tile
   if (!dev_check(args.M > 0 && args.N > 0 && args.nkb > 0 && args.group_m >= 1 && args.lora_k16 >= 0 &&
-                     args.lora_k16 <= 4,
+                     args.lora_k16 <= 4 && args.splits >= 1 && args.splits <= args.nkb,
                  args.status)) {
     grid_dep_wait();
     return;
@@ -104,8 +110,8 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::S + s); };
   const uint32_t acc_full0 = bar0 + 8u * (2 * C::S);
-  const uint32_t acc_empty0 = acc_full0 + 16u;
-  const uint32_t drain_bar = acc_full0 + 32u;
+  const uint32_t acc_empty0 = acc_full0 + 8u * C::ACCS;
+  const uint32_t drain_bar = acc_empty0 + 8u * C::ACCS;
   float* const scales = reinterpret_cast<float*>(sgen + C::OFF_SC);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sgen + C::OFF_BAR + C::NBAR * 8);
 
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
       mbar_init(full_bar(s), 3);  // the loads, and each CTA's scales
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < C::ACCS; ++b) {
       mbar_init(acc_full0 + 8u * b, 1);
       mbar_init(acc_empty0 + 8u * b, 2 * C::EPI_WARPS);
     }
@@ -133,14 +139,19 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  // tiles in groups of group_m row tiles, rows fastest inside a group (as the bf16 GEMM)
-  auto tile_coords = [&](int t, int& m0, int& n0) {
+  // Tiles in groups of group_m row tiles, rows fastest inside a group (as the bf16 GEMM); a tile's
+  // parts side by side.  Blocks [k0, k1) of the reduction; the last part takes the LoRA block (nkb).
+  auto unit_coords = [&](int u, int& m0, int& n0, int& k0, int& k1) {
+    const int t = u / args.splits, p = u - t * args.splits;
     const int gsz = args.group_m * n_tiles;
     const int first = (t / gsz) * args.group_m;
     const int gm = min(m_tiles - first, args.group_m);
     const int r = t - (first / args.group_m) * gsz;
     m0 = (first + r % gm) * 2 * C::BM + static_cast<int>(rank) * C::BM;
     n0 = (r / gm) * C::BNT;
+    k0 = static_cast<int>(static_cast<int64_t>(args.nkb) * p / args.splits);
+    k1 = static_cast<int>(static_cast<int64_t>(args.nkb) * (p + 1) / args.splits);
+    if (p == args.splits - 1 && args.lora_k16 > 0) ++k1;
   };
 
   if (warp < C::EPI_WARP0) {
@@ -150,32 +161,31 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
       bool ok = true;
       int s = 0;
       uint32_t ph = 1;
-      for (int t = cluster; t < total_tiles && ok; t += clusters) {
-        int m0, n0;
-        tile_coords(t, m0, n0);
+      for (int u = cluster; u < units && ok; u += clusters) {
+        int m0, n0, k0, k1;
+        unit_coords(u, m0, n0, k0, k1);
         const int col = n0 + static_cast<int>(rank) * C::BNC;  // this CTA's share of the tile's columns
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, args.status));
           if (!ok) break;
           if (elect_one()) {
             // both CTAs' loads complete on the leader's barrier
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 4 * C::TILE);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * (C::A_BYTES + C::B_BYTES));
             const uint32_t bar = lead0 + 8u * s;
-            const uint32_t a = sbase + C::OFF_A + s * C::TILE, b = sbase + C::OFF_B + s * C::TILE;
+            const uint32_t a = sbase + C::OFF_A + s * C::A_BYTES, b = sbase + C::OFF_B + s * C::B_BYTES;
             if (kb < args.nkb) {
               tma_load_2d_pair(a, &maps.a, bar, kb * C::BK, m0);
               // W rows x reduction bytes (K-major), or reduction rows x output columns (MN-major)
               if (BWD) tma_load_2d_pair(b, &maps.b, bar, col, kb * C::BK);
               else tma_load_2d_pair(b, &maps.b, bar, kb * C::BK, col);
             } else {
-              // LoRA operands, 64 wide with zeros beyond the rank: A [128 columns, r] K-major (dX), or
-              // B [r, 128 columns] MN-major in chunks of 64 columns (forward)
+              // LoRA operands, 64 wide with zeros beyond the rank: A [BNC columns, r] K-major (dX), or
+              // B [r, BNC columns] MN-major in chunks of 64 columns (forward)
               tma_load_2d_pair(a, &maps.la, bar, 0, m0);
               if (BWD) {
                 tma_load_2d_pair(b, &maps.lb, bar, 0, col);
               } else {
-                tma_load_2d_pair(b, &maps.lb, bar, col, 0);
-                tma_load_2d_pair(b + 8192, &maps.lb, bar, col + 64, 0);
+                for (int c = 0; c < C::BNC / 64; ++c) tma_load_2d_pair(b + c * 8192, &maps.lb, bar, col + c * 64, 0);
               }
             }
           }
@@ -191,34 +201,37 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
       constexpr uint32_t idesc = idesc_e4m3(2 * C::BM, C::BNT, false, BWD);
       constexpr uint32_t idesc_lora = idesc_bf16(2 * C::BM, C::BNT, false, !BWD);
       const uint64_t ad0 = smem_desc(sbase + C::OFF_A, 16, 1024, QL_SWZ_128B);
-      const uint64_t bd0 = smem_desc(sbase + C::OFF_B, BWD ? C::TILE : 16, 1024, QL_SWZ_128B);
+      // W for dX: reduction rows of BNC bytes (MN-major, one swizzle atom wide)
+      const uint64_t bd0 = BWD ? smem_desc(sbase + C::OFF_B, C::B_BYTES, 8 * C::BNC, C::BNC == 128 ? QL_SWZ_128B : QL_SWZ_64B)
+                               : smem_desc(sbase + C::OFF_B, 16, 1024, QL_SWZ_128B);
       const uint64_t bl0 = smem_desc(sbase + C::OFF_B, BWD ? 16 : 8192, 1024, QL_SWZ_128B);
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 1;  // phases of the operand ring and of the accumulators
-      for (int t = cluster; t < total_tiles && ok; t += clusters) {
-        for (int kb = 0; kb < blocks; ++kb) {
+      for (int u = cluster; u < units && ok; u += clusters) {
+        int m0, n0, k0, k1;
+        unit_coords(u, m0, n0, k0, k1);
+        for (int kb = k0; kb < k1; ++kb) {
           ok = mbar_wait(full_bar(s), ph, args.status) && mbar_wait(acc_empty0 + 8u * b, aph, args.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t acc = tmem + b * C::BNT;
-            const uint64_t so = static_cast<uint64_t>(s) * (C::TILE >> 4);
+            const uint64_t ao = static_cast<uint64_t>(s) * (C::A_BYTES >> 4), bo = static_cast<uint64_t>(s) * (C::B_BYTES >> 4);
             if (kb < args.nkb) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)  // 32 reduction elements each
-                umma_e4m3<2>(acc, ad0 + so + kk * 2, bd0 + so + kk * (BWD ? 256 : 2), idesc, kk != 0);
+                umma_e4m3<2>(acc, ad0 + ao + kk * 2, bd0 + bo + kk * (BWD ? 2 * C::BNC : 2), idesc, kk != 0);
             } else {
               for (int kk = 0; kk < args.lora_k16; ++kk)
-                umma_bf16<2>(acc, ad0 + so + kk * 2, bl0 + so + kk * (BWD ? 2 : 128), idesc_lora, kk != 0);
+                umma_bf16<2>(acc, ad0 + ao + kk * 2, bl0 + bo + kk * (BWD ? 2 : 128), idesc_lora, kk != 0);
             }
             umma_commit<2>(empty_bar(s));
             umma_commit<2>(acc_full0 + 8u * b);
           }
           __syncwarp();
           if (++s == C::S) s = 0, ph ^= 1;
-          aph ^= b;
-          b ^= 1;
+          if (++b == C::ACCS) b = 0, aph ^= 1;
         }
       }
       // let every issued MMA finish before TMEM can be released (after an error too)
@@ -233,12 +246,12 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
       bool ok = true;
       int s = 0, sl = 0;
       uint32_t ph = 1;
-      for (int t = cluster; t < total_tiles && ok; t += clusters) {
-        int m0, n0;
-        tile_coords(t, m0, n0);
+      for (int u = cluster; u < units && ok; u += clusters) {
+        int m0, n0, k0, k1;
+        unit_coords(u, m0, n0, k0, k1);
         const int nb = min(n0 / 128 + (lane & 1), (args.N - 1) / 128);
         const float* sb = args.sb + static_cast<size_t>(nb) * args.sb_n;
-        for (int kb = 0; kb < blocks && ok; kb += C::G) {
+        for (int kb = k0; kb < k1 && ok; kb += C::G) {
           float va[C::G][4];
 #pragma unroll
           for (int g = 0; g < C::G; ++g)
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
           const float vb = lane < 2 * C::G && kw < args.nkb ? __ldg(sb + static_cast<size_t>(kw) * args.sb_k) : 1.f;
 #pragma unroll
           for (int g = 0; g < C::G; ++g) {
-            if (kb + g >= blocks) break;
+            if (kb + g >= k1) break;
             ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, args.status));
             if (!ok) break;
             const float w0 = __shfl_sync(0xffffffffu, vb, 2 * g), w1 = __shfl_sync(0xffffffffu, vb, 2 * g + 1);
@@ -261,7 +274,7 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               d[i * 32] = va[g][i] * w0;
-              d[C::BM + i * 32] = va[g][i] * w1;
+              if constexpr (C::NBLK == 2) d[C::BM + i * 32] = va[g][i] * w1;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead0 + 8u * s);
@@ -276,21 +289,21 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
     setmaxnreg_inc<C::REGS_EPI>();
     const int ew = warp - C::EPI_WARP0;
     const int lg = warp & 3;    // TMEM lane quadrant this warp may access
-    const int half = ew >> 2;   // its 128 columns of the tile: one weight scale per reduction block
+    const int half = ew >> 2;   // its BNC columns of the tile: one weight scale per reduction block
     const uint32_t stg = sbase + C::OFF_EPI + ew * C::EPI_SLOT;
     uint8_t* stg_g = sgen + C::OFF_EPI + ew * C::EPI_SLOT;
     const uint64_t pol = l2_policy_evict_first();
-    const float* my_scale = scales + half * C::BM + lg * 32 + lane;
+    const float* my_scale = scales + (C::NBLK == 2 ? half * C::BM : 0) + lg * 32 + lane;
     int b = 0, sl = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int t = cluster; t < total_tiles && ok; t += clusters) {
-      int m0, n0;
-      tile_coords(t, m0, n0);
+    for (int u = cluster; u < units && ok; u += clusters) {
+      int m0, n0, k0, k1;
+      unit_coords(u, m0, n0, k0, k1);
       float acc[C::BNC];
 #pragma unroll
       for (int i = 0; i < C::BNC; ++i) acc[i] = 0.f;
-      for (int kb = 0; kb < blocks; ++kb) {
+      for (int kb = k0; kb < k1; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full0 + 8u * b, ph, args.status));
         if (!ok) break;
         tc_fence_after();
@@ -300,9 +313,9 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
         uint32_t v[2][32];  // 32 columns are loaded while the previous 32 are added
         tmem_ld_32x32b_x32_async(tacc, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < C::BNC / 32; ++c) {
           tmem_wait_ld(v[c & 1]);
-          if (c < 3) {
+          if (c + 1 < C::BNC / 32) {
             tmem_ld_32x32b_x32_async(tacc + (c + 1) * 32, v[(c + 1) & 1]);
           } else {  // every value is in registers: the MMA may have the accumulator back
             tc_fence_before();
@@ -312,13 +325,39 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(v[c & 1][i]), sc, acc[c * 32 + i]);
         }
-        ph ^= b;
-        b ^= 1;
+        if (++b == C::ACCS) b = 0, ph ^= 1;
       }
       if (!ok) break;
+      if (args.splits > 1) {
+        // a part's fp32 sums, in 16 x 32 chunks (128B swizzle) into its own rows of the partials
+        const int prow = (u % args.splits) * args.prows + m0 + lg * 32;
+#pragma unroll
+        for (int c = 0; c < C::BNC / 32; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+            if ((lane >> 4) == h) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float* v = acc + c * 32 + q * 4;
+                *reinterpret_cast<float4*>(stg_g + (lane & 15) * 128 + ((q ^ (lane & 7)) << 4)) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&maps.part, stg, n0 + half * C::BNC + c * 32, prow + h * 16, pol);
+              bulk_commit_group();
+            }
+          }
+        }
+        continue;
+      }
       // 32 x 32 chunks through this warp's shared slot (64B swizzle); the TMA store clips at the edges
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < C::BNC / 32; ++c) {
         if (lane == 0) bulk_wait_group_read<0>();  // the previous chunk's store has read the slot
         __syncwarp();
 #pragma unroll
@@ -349,10 +388,10 @@ __global__ void __launch_bounds__(Gemm8Cfg::THREADS, 1)
   }
 }
 
-template <bool BWD>
+template <bool BWD, int BN>
 static cudaError_t launch_one8(const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream) {
-  using C = Gemm8Cfg;
-  auto kern = gemm_fp8_kernel<BWD>;
+  using C = Gemm8Cfg<BN>;
+  auto kern = gemm_fp8_kernel<BWD, BN>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -384,14 +423,41 @@ static cudaError_t launch_one8(const Gemm8Maps& maps, const Gemm8Args& args, cud
     cudaGetLastError();
     resident[dev] = n * 2;
   }
-  const int total = ((args.M + 255) / 256) * ((args.N + 255) / 256);
+  const int total = ((args.M + 255) / 256) * ((args.N + BN - 1) / BN) * args.splits;
   const int ctas = apply_grid_cap(total * 2 < resident[dev] ? total * 2 : resident[dev], 2);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
-cudaError_t launch_gemm_fp8(bool bwd, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream) {
-  return bwd ? launch_one8<true>(maps, args, stream) : launch_one8<false>(maps, args, stream);
+// out[m, n] = sum of the parts in order; eight columns per thread.
+__global__ void __launch_bounds__(256) gemm_fp8_sum_kernel(const float* __restrict__ part, int64_t prows, int splits,
+                                                           int64_t N, int64_t total, bf16* __restrict__ out) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= total) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(part + s * prows * N + i);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  *reinterpret_cast<uint4*>(out + i) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
+                                cudaStream_t st) {
+  return launch_pdl(gemm_fp8_sum_kernel, dim3(static_cast<unsigned>((M * N / 8 + 255) / 256)), dim3(256), 0, st, part,
+                    prows, splits, N, M * N, out);
+}
+
+// bn: output columns per tile (256 or 128); the tensor maps' boxes follow it.
+cudaError_t launch_gemm_fp8(bool bwd, int bn, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream) {
+  if (bn == 256) return bwd ? launch_one8<true, 256>(maps, args, stream) : launch_one8<false, 256>(maps, args, stream);
+  if (bn == 128) return bwd ? launch_one8<true, 128>(maps, args, stream) : launch_one8<false, 128>(maps, args, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace ql

@@ -71,10 +71,11 @@ struct GemmArgs {
 // row and 128 reduction columns, W one per 128 x 128 block.
 struct Gemm8Maps {
   CUtensorMap a;    // A operand: e4m3 [M, reduction], box {128, 128}, 128B swizzle
-  CUtensorMap b;    // weight: e4m3 [n_out, k_in], box {128, 128}, 128B swizzle
+  CUtensorMap b;    // weight: e4m3 [n_out, k_in], box {128, bn / 2}, 128B swizzle (forward), or {bn / 2, 128} (dX)
   CUtensorMap la;   // LoRA left operand s*XA or s*G: bf16 [M, r], box {64, 128}
-  CUtensorMap lb;   // LoRA right operand: B [r, N] (forward), box {64, 64}, or A [N, r] (dX), box {64, 128}
+  CUtensorMap lb;   // LoRA right operand: B [r, N] (forward), box {64, 64}, or A [N, r] (dX), box {64, bn / 2}
   CUtensorMap out;  // output: bf16 [M, N], box {32, 32}, 64B swizzle
+  CUtensorMap part; // splits > 1: fp32 [splits * prows, N], box {32, 16}, 128B swizzle
 };
 struct Gemm8Args {
   int M, N;             // output rows and columns
@@ -85,6 +86,8 @@ struct Gemm8Args {
   int sb_k, sb_n;       // their strides per reduction block and per 128 output columns
   int* status;          // device status word (timeouts)
   int group_m;          // tile order, as GemmArgs
+  int splits;           // parts of the reduction (1: the tile is stored as bf16)
+  int prows;            // rows of a part's partials (M rounded up to whole tiles)
 };
 
 // --------------------------------------------------------------- skinny ---

@@ -89,7 +89,10 @@ def _values(x, sx, w, sw):
 
 
 MM_SHAPES = [(1, 64, 16), (1, 4096, 4096), (3, 16, 16), (16, 1024, 512), (17, 144, 272), (64, 512, 128), (128, 256, 384),
-             (130, 1040, 528), (200, 2048, 144), (256, 128, 256), (257, 400, 2064), (520, 384, 1552), (1025, 272, 640)]
+             (130, 1040, 528), (200, 2048, 144), (256, 128, 256), (257, 400, 2064), (520, 384, 1552), (1025, 272, 640),
+             # 17 to 32 rows; parts of a long reduction, in both directions; tiles of 256 columns, in both directions
+             (20, 528, 400), (32, 2048, 1040), (70, 4096, 80), (130, 144, 2064), (300, 80, 6160), (33, 1552, 16),
+             (2050, 272, 1296), (2050, 1296, 272), (1300, 144, 2064), (4000, 80, 656)]
 
 
 @pytest.mark.parametrize("bwd", [False, True])
@@ -110,9 +113,10 @@ def test_matmul(M, K, N, bwd):
 
 
 @pytest.mark.parametrize("bwd", [False, True])
-def test_matmul_few_ctas(bwd):
-    """Every CTA walks many tiles (rings and accumulators wrap), with the same result."""
-    M, K, N = 700, 640, 1296
+@pytest.mark.parametrize("M,K,N", [(700, 640, 1296), (130, 1680, 1680), (2100, 1200, 1300 // 16 * 16)])
+def test_matmul_few_ctas(M, K, N, bwd):
+    """Every CTA walks many tiles (rings and accumulators wrap), with the same result: tiles of 128 columns, parts of
+    a reduction, tiles of 256 columns."""
     red = N if bwd else K
     x, sx, w, sw = _operands(M, K, N, red, 5)
     xg, wg = ops.FP8Rows(x.cuda(), sx.cuda()), ops.FP8Weight(w.cuda(), sw.cuda())
@@ -129,7 +133,7 @@ def test_matmul_few_ctas(bwd):
     assert np.all(np.abs(gpu_f64(full) - ref) <= U16 * np.abs(ref) + 1.01 * _mma_slack(red) * (np.abs(xv) @ np.abs(op)))
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 30, 40, 300])
 @pytest.mark.parametrize("bwd", [False, True])
 def test_matmul_row_with_nan_spoils_itself_only(M, bwd):
     K, N = 400, 272
@@ -149,9 +153,9 @@ def test_matmul_row_with_nan_spoils_itself_only(M, bwd):
     assert not torch.isfinite(out[M // 2]).any() and torch.equal(out[others], good[others])
 
 
-@pytest.mark.parametrize("M", [1, 60, 600])
+@pytest.mark.parametrize("M", [1, 25, 60, 600, 3000])
 def test_matmul_repeats_bit_for_bit(M):
-    x, sx, w, sw = _operands(M, 1024, 528, 1024, 7)
+    x, sx, w, sw = _operands(M, 1600, 1040, 1600, 7)
     xg, wg, ws = ops.FP8Rows(x.cuda(), sx.cuda()), ops.FP8Weight(w.cuda(), sw.cuda()), ops.Workspace()
     first = ops.fp8_matmul(xg, wg, ws)
     for _ in range(5):
@@ -170,7 +174,8 @@ def _linear(M, K, N, r, s, seed):
 
 
 LIN_SHAPES = [(1, 64, 16, 16, 1.0), (1, 1024, 528, 64, 0.25), (64, 4096, 1024, 64, 0.25), (130, 400, 272, 16, 2.0),
-              (300, 512, 1040, 32, 0.5), (1030, 272, 384, 16, 1.0), (257, 1040, 2064, 64, 1.7)]
+              (300, 512, 1040, 32, 0.5), (1030, 272, 384, 16, 1.0), (257, 1040, 2064, 64, 1.7),
+              (20, 512, 400, 32, 0.5), (33, 1680, 144, 16, 1.0), (90, 144, 1680, 64, 0.25), (2050, 1296, 1296, 32, 0.5)]
 
 
 @pytest.mark.parametrize("M,K,N,r,s", LIN_SHAPES)
