@@ -1553,9 +1553,11 @@ qlora_status fp8_matmul_t(const qlora_fp8_rows* dY, const qlora_fp8* w, int64_t 
 }
 
 namespace {
-// Workspace of an e4m3 projection: [status word | 256 B][M x r vector][row codes][row scales][partials]
+// Workspace of an e4m3 projection: [status word | 256 B][M x r vector][row codes][row scales][partials].
+// At ranks 32 and 64 the backward reduces its dB and dA passes in one launch at the end, so their
+// partials stay apart from those of the passes between: [dB][dA][the rest].
 struct Linear8Ws {
-  size_t vec, codes, scale, part, total;
+  size_t vec, codes, scale, db, da, part, total;
 };
 Linear8Ws linear8_ws(int64_t M, int64_t K, int64_t N, int r) {
   Linear8Ws w;
@@ -1563,7 +1565,9 @@ Linear8Ws linear8_ws(int64_t M, int64_t K, int64_t N, int r) {
   w.vec = 256;
   w.codes = w.vec + align256(static_cast<size_t>(M) * r * 2);
   w.scale = w.codes + align256(static_cast<size_t>(M) * wide);
-  w.part = w.scale + align256(static_cast<size_t>(M) * cdiv(wide, 128) * 4);
+  w.db = w.scale + align256(static_cast<size_t>(M) * cdiv(wide, 128) * 4);
+  w.da = w.db + (r == 16 ? 0 : align256(colproj_part_bytes(M, N, r)));
+  w.part = w.da + (r == 16 ? 0 : align256(colproj_part_bytes(M, K, r)));
   size_t part = rowproj_part_bytes(M, K, r);
   part = std::max(part, dypass_part_bytes(M, N, r));
   part = std::max(part, colproj_part_bytes(M, K, r));
@@ -1650,16 +1654,27 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
   float* part = reinterpret_cast<float*>(w + l.part);
   const float sc = lin->scale;
   if ((s = fp8_quantize_rows(dY, M, N, codes, scale, stream)) != QLORA_OK) return s;
+  const bf16 *dy = reinterpret_cast<const bf16*>(dY), *x = reinterpret_cast<const bf16*>(X);
+  const bf16* xa = reinterpret_cast<const bf16*>(XA_saved);
+  const ReduceOuts gouts = routs(rout(sG, 0, r, r, 0, sc));
+  const ReduceOuts bouts = routs(rout(reinterpret_cast<bf16*>(dB), 0, r, (int)N, 1, sc));
+  const ReduceOuts aouts = routs(rout(reinterpret_cast<bf16*>(dA), 0, r, r, 0, 1.f));
   // G = dY B^T (stored scaled), dB = s (X A)^T dY, from the unquantised dY
-  s = pass_dypass(reinterpret_cast<const bf16*>(dY), M, N, reinterpret_cast<const bf16*>(XA_saved),
-                  reinterpret_cast<const bf16*>(lin->B), r, part, routs(rout(sG, 0, r, r, 0, sc)),
-                  routs(rout(reinterpret_cast<bf16*>(dB), 0, r, (int)N, 1, sc)), status, st);
+  ReduceBatch rb;
+  if (r == 16) {
+    s = pass_dypass(dy, M, N, xa, reinterpret_cast<const bf16*>(lin->B), r, part, gouts, bouts, status, st);
+  } else {
+    s = pass_rowproj_bt(dy, M, N, reinterpret_cast<const bf16*>(lin->B), r, part, gouts, status, st);
+    if (s != QLORA_OK) return s;
+    s = pass_colproj(dy, M, N, xa, r, reinterpret_cast<float*>(w + l.db), bouts, status, st, 0, 0, &rb);
+  }
   if (s != QLORA_OK) return s;
   s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG, reinterpret_cast<const bf16*>(lin->A),
                r, part, status, st);
   if (s != QLORA_OK) return s;
-  return pass_colproj(reinterpret_cast<const bf16*>(X), M, K, sG, r, part,
-                      routs(rout(reinterpret_cast<bf16*>(dA), 0, r, r, 0, 1.f)), status, st);
+  if (r == 16) return pass_colproj(x, M, K, sG, r, part, aouts, status, st);
+  s = pass_colproj(x, M, K, sG, r, reinterpret_cast<float*>(w + l.da), aouts, status, st, 0, 0, &rb);
+  return s != QLORA_OK ? s : flush_reduce(rb, st);
 }
 
 // NF4 entry points: the current tile configuration.

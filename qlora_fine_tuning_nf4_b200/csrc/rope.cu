@@ -9,15 +9,19 @@
 // where a binary32 product would be off by whole radians; no 64-bit floating point
 // and no table of cosines per position is needed.
 //
-// HBM-bound.  A CTA takes a few tokens: its threads first find each token's
-// cosines and sines once (shared memory), then stream all its heads, a thread
-// keeping its pairs' factors in registers across them.
+// HBM-bound.  A CTA takes one or two tokens: its threads find each token's cosines
+// and sines once (shared memory) while their first loads are on the way, then
+// stream the heads.  Many small CTAs with 32 registers a thread (16 of 128 threads
+// per SM) keep more bytes in flight than longer batches per thread: 8192 tokens of
+// 40 heads of 128 in rows of 6144, 168 MB, take 30.6 us (5.5 TB/s); with 256
+// threads, four tokens and two heads in flight per thread (72 registers) 36.5 us,
+// with the loads of a head after the previous head's store 45 us.
 #include "fp8.cuh"
 
 namespace ql {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TOK = 4;       // tokens per CTA at most
+constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_TOK = 2;       // tokens per CTA at most
 constexpr int ROPE_MAX_D = 512;   // widest head
 
 struct RopeArgs {
@@ -27,7 +31,7 @@ struct RopeArgs {
   const int64_t* pos;   // [M], or null: row (modulo seq_len if that is positive)
   int64_t ldx, ldo, seq_len;
   int M, heads, D, rot;
-  int tok, hsplit;      // tokens per CTA; CTAs that share a token group's heads
+  int tok;              // tokens per CTA
   float factor, sign;   // cos and sin are multiplied by factor; sign -1: transposed
 };
 
@@ -68,73 +72,87 @@ QL_DEV typename RopeVec<VEC>::T rope_pack(const float (&f)[VEC]) {
 // VEC (copied where out is not X).  A rotated item is VEC pairs read as two
 // vectors (halves), or VEC / 2 pairs in one (interleaved).
 template <bool INTER, int VEC>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_THREADS, 16) rope_kernel(const RopeArgs a) {
   using V = typename RopeVec<VEC>::T;
   constexpr int NP = INTER ? VEC / 2 : VEC;  // pairs per item
+  constexpr int HB = INTER ? 2 : 1;          // items in flight per thread
   __shared__ float2 cs[ROPE_TOK * ROPE_MAX_D / 2];
   grid_dep_wait();
   grid_dep_launch();
   const int half = a.rot / 2;
-  const int row0 = static_cast<int>(blockIdx.x / a.hsplit) * a.tok;
+  const int row0 = static_cast<int>(blockIdx.x) * a.tok;
   const int ntok = min(a.tok, a.M - row0);
+  const int np = half / NP;
+  const int items = np + (a.out == a.X ? 0 : (a.D - a.rot) / VEC);
+  const int lanes = min(items, ROPE_THREADS);
+  const int hl = threadIdx.x / lanes, nh = ROPE_THREADS / lanes;  // nh heads (of any tokens) side by side
+  const int v0 = threadIdx.x % lanes;
+  const int total = hl < nh ? ntok * a.heads : 0;
+  const bf16* X = a.X + static_cast<size_t>(row0) * a.ldx;
+  bf16* O = a.out + static_cast<size_t>(row0) * a.ldo;
+  V p[HB], q[HB];
+  int tk[HB], hd[HB];
+  // HB (token, head) items' loads are in flight before the first store: X and out may be the same
+  // memory, so the compiler cannot move a later load up
+  auto load = [&](int v, int i0) {
+    const int e = v >= np ? a.rot + (v - np) * VEC : v * VEC;
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      const int i = i0 + j * nh;
+      tk[j] = i / a.heads;
+      hd[j] = i - tk[j] * a.heads;
+      if (i < total) {
+        const bf16* x = X + tk[j] * a.ldx + hd[j] * a.D + e;
+        p[j] = *reinterpret_cast<const V*>(x);
+        if (!INTER && v < np) q[j] = *reinterpret_cast<const V*>(x + half);
+      }
+    }
+  };
+  load(v0, hl);  // on its way while the angles are found
   for (int i = threadIdx.x; i < ntok * half; i += ROPE_THREADS) {
     const int64_t row = row0 + i / half;
-    const int64_t p = a.pos ? a.pos[row] : (a.seq_len > 0 ? row % a.seq_len : row);
-    const uint64_t t = static_cast<uint64_t>(p) * a.turns[i % half];
+    const int64_t pos = a.pos ? a.pos[row] : (a.seq_len > 0 ? row % a.seq_len : row);
+    const uint64_t t = static_cast<uint64_t>(pos) * a.turns[i % half];
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
     cs[i] = make_float2(c * a.factor, s * a.factor * a.sign);
   }
   __syncthreads();
-  const int np = half / NP;
-  const int items = np + (a.out == a.X ? 0 : (a.D - a.rot) / VEC);
-  const int lanes = min(items, ROPE_THREADS);
-  const int hl = threadIdx.x / lanes, nh = ROPE_THREADS / lanes;
-  const int h0 = static_cast<int>(blockIdx.x % a.hsplit) * nh + hl, hstep = nh * a.hsplit;
-  if (hl >= nh) return;
-  for (int v = threadIdx.x % lanes; v < items; v += lanes) {
-    for (int k = 0; k < ntok; ++k) {
-      const bf16* x = a.X + static_cast<size_t>(row0 + k) * a.ldx;
-      bf16* o = a.out + static_cast<size_t>(row0 + k) * a.ldo;
-      if (v >= np) {
-        const int e = a.rot + (v - np) * VEC;
-#pragma unroll 4
-        for (int h = h0; h < a.heads; h += hstep)
-          *reinterpret_cast<V*>(o + h * a.D + e) = *reinterpret_cast<const V*>(x + h * a.D + e);
-        continue;
-      }
-      float2 f[NP];
+  for (int v = v0; v < items; v += lanes) {
+    const bool tail = v >= np;
+    const int e = tail ? a.rot + (v - np) * VEC : v * VEC;
+    if (v != v0) load(v, hl);
+    for (int i0 = hl; i0 < total; i0 += HB * nh) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) f[i] = cs[k * half + v * NP + i];
-      if constexpr (INTER) {
-#pragma unroll 4
-        for (int h = h0; h < a.heads; h += hstep) {
-          float r[VEC];
-          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + v * VEC), r);
+      for (int j = 0; j < HB; ++j) {
+        if (i0 + j * nh >= total) break;
+        bf16* o = O + tk[j] * a.ldo + hd[j] * a.D + e;
+        if (!tail) {
+          const float2* f = cs + tk[j] * half + v * NP;
+          float r[VEC], t[VEC];
+          rope_unpack<VEC>(p[j], r);
+          if constexpr (INTER) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const float p = r[2 * i], q = r[2 * i + 1];
-            r[2 * i] = p * f[i].x - q * f[i].y;
-            r[2 * i + 1] = q * f[i].x + p * f[i].y;
+            for (int i = 0; i < NP; ++i) {
+              const float u = r[2 * i], w = r[2 * i + 1];
+              r[2 * i] = u * f[i].x - w * f[i].y;
+              r[2 * i + 1] = w * f[i].x + u * f[i].y;
+            }
+          } else {
+            rope_unpack<VEC>(q[j], t);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float u = r[i] * f[i].x - t[i] * f[i].y;
+              t[i] = t[i] * f[i].x + r[i] * f[i].y;
+              r[i] = u;
+            }
+            *reinterpret_cast<V*>(o + half) = rope_pack<VEC>(t);
           }
-          *reinterpret_cast<V*>(o + h * a.D + v * VEC) = rope_pack<VEC>(r);
+          p[j] = rope_pack<VEC>(r);
         }
-      } else {
-#pragma unroll 4
-        for (int h = h0; h < a.heads; h += hstep) {
-          float p[VEC], q[VEC];
-          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + v * VEC), p);
-          rope_unpack<VEC>(*reinterpret_cast<const V*>(x + h * a.D + half + v * VEC), q);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float u = p[i] * f[i].x - q[i] * f[i].y;
-            q[i] = q[i] * f[i].x + p[i] * f[i].y;
-            p[i] = u;
-          }
-          *reinterpret_cast<V*>(o + h * a.D + v * VEC) = rope_pack<VEC>(p);
-          *reinterpret_cast<V*>(o + h * a.D + half + v * VEC) = rope_pack<VEC>(q);
-        }
+        *reinterpret_cast<V*>(o) = p[j];
       }
+      if (i0 + HB * nh < total) load(v, i0 + HB * nh);
     }
   }
 }
@@ -142,9 +160,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeArgs a) {
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
                         int64_t ldo, cudaStream_t st) {
-  RopeArgs a = {X, out, turns, pos, ldx, ldo, seq_len, (int)M, heads, D, rot, 1, 1, factor, transpose ? -1.f : 1.f};
-  a.tok = ROPE_TOK;
-  const unsigned grid = static_cast<unsigned>((M + a.tok - 1) / a.tok * a.hsplit);
+  RopeArgs a = {X, out, turns, pos, ldx, ldo, seq_len, (int)M, heads, D, rot, 1, factor, transpose ? -1.f : 1.f};
+  a.tok = M >= 4 * 148 * ROPE_TOK ? ROPE_TOK : 1;
+  const unsigned grid = static_cast<unsigned>((M + a.tok - 1) / a.tok);
 #define QL_ROPE(I_, V_) launch_pdl(rope_kernel<I_, V_>, dim3(grid), dim3(ROPE_THREADS), 0, st, a)
   // the widest vector that divides the rotated part: heads start on 16 bytes (D % 8 == 0)
   if (interleaved) {

@@ -283,7 +283,7 @@ def _t(t, name, shape, dtype=torch.bfloat16):
     """Marshalling check of one tensor argument: contiguous, on the current
     CUDA device, of the expected dtype and shape.  The C ABI only sees raw
     pointers, so a host tensor or a short buffer must be caught here."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
             and t.get_device() == _current_device()):
         return t
     if not isinstance(t, torch.Tensor):
@@ -397,15 +397,25 @@ def _dims(lin):
 
 
 class Workspace:
-    """Caller-owned device workspace (zeroed once; grows on demand)."""
+    """Caller-owned device workspace (zeroed once; grows on demand).
+
+    One workspace serves calls whose GPU work does not overlap: calls on one stream, or graphs replayed one after
+    the other.  Streams that run at the same time need one each.  A buffer that calls were captured with stays
+    alive after the workspace has grown, since a graph's replay still uses it."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.zeros(256, dtype=torch.uint8, device=device)
+        self.captured, self.kept = False, []
 
     def get(self, nbytes):
         if self.buf.numel() < nbytes:
+            if self.captured:
+                self.kept.append(self.buf)
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self.captured = False
+        if not self.captured and torch.cuda.is_current_stream_capturing():
+            self.captured = True
         return self.buf
 
 
@@ -703,16 +713,18 @@ class FP8Weight:
         return self.codes.shape[1]
 
     def c(self):
-        if not isinstance(self.codes, torch.Tensor) or self.codes.dim() != 2:
+        codes, scale = self.codes, self.scale
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
             raise ValueError("codes must be a 2-D float8_e4m3fn tensor [n_out, k_in]")
-        _t(self.codes, "codes", tuple(self.codes.shape), torch.float8_e4m3fn)
-        _t(self.scale, "scale", (_blocks(self.n_out), _blocks(self.k_in)), torch.float32)
-        return QloraFP8(self.codes.data_ptr(), self.scale.data_ptr(), self.n_out, self.k_in)
+        n, k = codes.shape
+        _t(codes, "codes", (n, k), torch.float8_e4m3fn)
+        _t(scale, "scale", (_blocks(n), _blocks(k)), torch.float32)
+        return QloraFP8(codes.data_ptr(), scale.data_ptr(), n, k)
 
 
-def _empty_rows(M, K, device):
-    return FP8Rows(torch.empty(M, K, dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(_blocks(K), M, dtype=torch.float32, device=device))
+def _empty_rows(M, K, like):
+    return FP8Rows(like.new_empty((M, K), dtype=torch.float8_e4m3fn),
+                   like.new_empty((_blocks(K), M), dtype=torch.float32))
 
 
 def fp8_quantize_rows(X, out: FP8Rows = None):
@@ -720,7 +732,7 @@ def fp8_quantize_rows(X, out: FP8Rows = None):
     M, K = _rows(X)
     _t(X, "X", (M, K))
     if out is None:
-        out = _empty_rows(M, K, X.device)
+        out = _empty_rows(M, K, X)
     c = out.c("out", (M, K))
     _check("fp8_quantize_rows", lib().fp8_quantize_rows(_p(X), M, K, c.codes, c.scale, _stream()))
     return out
@@ -750,7 +762,8 @@ def _fp8_matmul(fn, x, w, ws, out, red, cols):
     cx = x.c("x", (M, red(w)))
     if out is None:
         out = torch.empty(M, cols(w), dtype=torch.bfloat16, device=x.codes.device)
-    _t(out, "out", (M, cols(w)))
+    else:
+        _t(out, "out", (M, cols(w)))
     buf = ws.get(fp8_matmul_workspace_bytes(M, w.k_in, w.n_out))
     _check(fn, getattr(lib(), fn)(ctypes.byref(cx), ctypes.byref(cw), M, _p(out), _p(buf), buf.numel(), _stream()))
     return out
@@ -791,13 +804,9 @@ def qlora_linear8_fwd(lin: LoraLinear8, X, ws: Workspace, Y=None, XA=None, X8: F
     M = _rows(X)[0]
     c = lin.c()
     n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
-    if Y is None:
-        Y = torch.empty(M, n_out, dtype=torch.bfloat16, device=X.device)
-    if XA is None:
-        XA = torch.empty(M, r, dtype=torch.bfloat16, device=X.device)
     _t(X, "X", (M, k_in))
-    _t(Y, "Y", (M, n_out))
-    _t(XA, "XA", (M, r))
+    Y = X.new_empty((M, n_out)) if Y is None else _t(Y, "Y", (M, n_out))
+    XA = X.new_empty((M, r)) if XA is None else _t(XA, "XA", (M, r))
     c8 = X8.c("X8", (M, k_in)) if X8 is not None else None
     buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
     _check("qlora_linear8_fwd", lib().qlora_linear8_fwd(ctypes.byref(c), _p(X), ctypes.byref(c8) if c8 else None, M,
@@ -809,18 +818,12 @@ def qlora_linear8_bwd(lin: LoraLinear8, X, XA, dY, ws: Workspace, dX=None, dA=No
     M = _rows(X)[0]
     c = lin.c()
     n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
-    if dX is None:
-        dX = torch.empty(M, k_in, dtype=torch.bfloat16, device=X.device)
-    if dA is None:
-        dA = torch.empty_like(lin.A)
-    if dB is None:
-        dB = torch.empty_like(lin.B)
     _t(X, "X", (M, k_in))
     _t(XA, "XA", (M, r))
     _t(dY, "dY", (M, n_out))
-    _t(dX, "dX", (M, k_in))
-    _t(dA, "dA", (k_in, r))
-    _t(dB, "dB", (r, n_out))
+    dX = X.new_empty((M, k_in)) if dX is None else _t(dX, "dX", (M, k_in))
+    dA = X.new_empty((k_in, r)) if dA is None else _t(dA, "dA", (k_in, r))
+    dB = X.new_empty((r, n_out)) if dB is None else _t(dB, "dB", (r, n_out))
     buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
     _check("qlora_linear8_bwd", lib().qlora_linear8_bwd(ctypes.byref(c), _p(X), _p(XA), _p(dY), M, _p(dX), _p(dA),
                                                         _p(dB), _p(buf), buf.numel(), _stream()))
@@ -842,20 +845,19 @@ def qlora_add_rmsnorm_fwd(X, R, w, eps, plus_one=False, H=None, Y=None, rstd=Non
             raise ValueError("H is X itself where R is None")
     else:
         _t(R, "R", (M, d))
-        if H is None:
-            H = torch.empty_like(X)
-        _t(H, "H", (M, d))
-    if want_y and Y is None:
-        Y = torch.empty_like(X)
+        H = torch.empty_like(X) if H is None else _t(H, "H", (M, d))
+    _t(w, "w", (d,))
     if Y is not None:
         _t(Y, "Y", (M, d))
-    if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=X.device)
-    if quantize and Y8 is None:
-        Y8 = _empty_rows(M, d, X.device)
-    _t(w, "w", (d,))
-    _t(rstd, "rstd", (M,), torch.float32)
-    c8 = Y8.c("Y8", (M, d)) if Y8 is not None else None
+    elif want_y:
+        Y = torch.empty_like(X)
+    rstd = X.new_empty((M,), dtype=torch.float32) if rstd is None else _t(rstd, "rstd", (M,), torch.float32)
+    c8 = None
+    if Y8 is not None:
+        c8 = Y8.c("Y8", (M, d))
+    elif quantize:
+        Y8 = _empty_rows(M, d, X)
+        c8 = QloraFP8Rows(Y8.codes.data_ptr(), Y8.scale.data_ptr())
     _check("qlora_add_rmsnorm_fwd", lib().qlora_add_rmsnorm_fwd(
         _p(X), _p(R), _p(w), M, d, float(eps), int(bool(plus_one)), _p(None if R is None else H), _p(Y),
         ctypes.byref(c8) if c8 else None, _p(rstd), _stream()))
@@ -865,15 +867,13 @@ def qlora_add_rmsnorm_fwd(X, R, w, eps, plus_one=False, H=None, Y=None, rstd=Non
 def qlora_add_rmsnorm_bwd(H, w, rstd, dY, dH=None, plus_one=False, dX=None):
     """Gradient of X and of R: dH (what reaches H past the norm) plus the norm's.  dX may be dY or dH."""
     M, d = _rows(H, "H")
-    if dX is None:
-        dX = torch.empty_like(H)
     _t(H, "H", (M, d))
     _t(w, "w", (d,))
     _t(rstd, "rstd", (M,), torch.float32)
     _t(dY, "dY", (M, d))
     if dH is not None:
         _t(dH, "dH", (M, d))
-    _t(dX, "dX", (M, d))
+    dX = torch.empty_like(H) if dX is None else _t(dX, "dX", (M, d))
     _check("qlora_add_rmsnorm_bwd", lib().qlora_add_rmsnorm_bwd(_p(H), _p(w), _p(rstd), _p(dY), _p(dH), M, d,
                                                                 int(bool(plus_one)), _p(dX), _stream()))
     return dX
@@ -966,7 +966,7 @@ def _rope_rows(t, name, cols):
         raise ValueError(f"{name} must have shape [M, {cols}], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
@@ -981,10 +981,11 @@ def _rope(fn, X, heads, head_dim, plan, positions, seq_len, interleaved, out):
     ldx = _rope_rows(X, "X", cols)
     M = X.shape[0]
     if out is None:
-        out = torch.empty(M, cols, dtype=torch.bfloat16, device=X.device)
-    ldo = _rope_rows(out, "out", cols)
-    if out.shape[0] != M:
-        raise ValueError(f"out must have {M} rows, got {out.shape[0]}")
+        out, ldo = X.new_empty((M, cols)), cols
+    else:
+        ldo = _rope_rows(out, "out", cols)
+        if out.shape[0] != M:
+            raise ValueError(f"out must have {M} rows, got {out.shape[0]}")
     if M > 0 and not (out.data_ptr() == X.data_ptr() and ldo == ldx):
         # in place, apart in memory, or other columns of the same rows
         a, b = X.data_ptr() // 2, out.data_ptr() // 2
