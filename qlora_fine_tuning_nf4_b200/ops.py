@@ -755,9 +755,9 @@ def fp8_matmul_workspace_bytes(M, K, N):
 def _fp8_matmul(fn, x, w, ws, out, red, cols):
     if not isinstance(x, FP8Rows) or not isinstance(w, FP8Weight):
         raise TypeError(f"{fn} takes FP8Rows and FP8Weight")
-    cw = w.c()
     if not isinstance(x.codes, torch.Tensor) or x.codes.dim() != 2:
         raise ValueError("x.codes must be a 2-D float8_e4m3fn tensor")
+    cw = w.c()
     M = x.codes.shape[0]
     cx = x.c("x", (M, red(w)))
     if out is None:
