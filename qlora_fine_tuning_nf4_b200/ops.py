@@ -839,11 +839,10 @@ def qlora_add_rmsnorm_fwd(X, R, w, eps, plus_one=False, H=None, Y=None, rstd=Non
     Y8 (FP8Rows of Y) is written with quantize=True or where it is given, else None; Y is None with
     want_y=False.  H may be X or R."""
     M, d = _rows(X)
+    if R is None and H is not None and H is not X:
+        raise ValueError("H is X itself where R is None")
     _t(X, "X", (M, d))
-    if R is None:
-        if H is not None and H is not X:
-            raise ValueError("H is X itself where R is None")
-    else:
+    if R is not None:
         _t(R, "R", (M, d))
         H = torch.empty_like(X) if H is None else _t(H, "H", (M, d))
     _t(w, "w", (d,))

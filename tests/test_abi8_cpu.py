@@ -158,7 +158,7 @@ def test_binding_rejects_before_any_library_call():
     with pytest.raises(TypeError):
         ops.fp8_matmul(rows, X, None)
     with pytest.raises(ValueError, match="2-D"):
-        ops.fp8_matmul(ops.FP8Rows(torch.zeros(8), torch.ones(1)), W, None)
+        ops.fp8_matmul(ops.FP8Rows(torch.zeros(8, dtype=torch.float8_e4m3fn), torch.ones(1)), W, None)
     with pytest.raises(ValueError, match="H is X"):
         ops.qlora_add_rmsnorm_fwd(X, None, w, 1e-5, H=torch.zeros_like(X))
     with pytest.raises(ValueError, match="shape"):
