@@ -748,35 +748,49 @@ def fp8_quantize(w):
     return q
 
 
+def _call_ws(fn, ws, need, args):
+    """One call that ends in (workspace, its bytes, stream).  The library checks the size before it enqueues anything,
+    so the size is asked for only when the workspace at hand is too small."""
+    f = getattr(lib(), fn)
+    buf = ws.get(0)
+    status = f(*args, buf.data_ptr(), buf.numel(), _stream())
+    if status == 4:  # QLORA_ERR_WORKSPACE_TOO_SMALL
+        buf = ws.get(need())
+        status = f(*args, buf.data_ptr(), buf.numel(), _stream())
+    _check(fn, status)
+
+
 def fp8_matmul_workspace_bytes(M, K, N):
     return int(lib().fp8_matmul_workspace_bytes(M, K, N))
 
 
-def _fp8_matmul(fn, x, w, ws, out, red, cols):
+def _fp8_matmul(fn, x, w, ws, out, transposed):
     if not isinstance(x, FP8Rows) or not isinstance(w, FP8Weight):
         raise TypeError(f"{fn} takes FP8Rows and FP8Weight")
     if not isinstance(x.codes, torch.Tensor) or x.codes.dim() != 2:
         raise ValueError("x.codes must be a 2-D float8_e4m3fn tensor")
     cw = w.c()
+    n_out, k_in = w.codes.shape
+    red, cols = (n_out, k_in) if transposed else (k_in, n_out)
     M = x.codes.shape[0]
-    cx = x.c("x", (M, red(w)))
+    cx = x.c("x", (M, red))
     if out is None:
-        out = torch.empty(M, cols(w), dtype=torch.bfloat16, device=x.codes.device)
+        out = torch.empty(M, cols, dtype=torch.bfloat16, device=x.codes.device)
     else:
-        _t(out, "out", (M, cols(w)))
-    buf = ws.get(fp8_matmul_workspace_bytes(M, w.k_in, w.n_out))
-    _check(fn, getattr(lib(), fn)(ctypes.byref(cx), ctypes.byref(cw), M, _p(out), _p(buf), buf.numel(), _stream()))
+        _t(out, "out", (M, cols))
+    _call_ws(fn, ws, lambda: fp8_matmul_workspace_bytes(M, k_in, n_out),
+             (ctypes.byref(cx), ctypes.byref(cw), M, out.data_ptr()))
     return out
 
 
 def fp8_matmul(x: FP8Rows, w: FP8Weight, ws: Workspace, Y=None):
     """Y = x W^T [M, n_out] in bf16 from x [M, k_in]."""
-    return _fp8_matmul("fp8_matmul", x, w, ws, Y, lambda w: w.k_in, lambda w: w.n_out)
+    return _fp8_matmul("fp8_matmul", x, w, ws, Y, False)
 
 
 def fp8_matmul_t(dY: FP8Rows, w: FP8Weight, ws: Workspace, dX=None):
     """dX = dY W [M, k_in] in bf16 from dY [M, n_out]."""
-    return _fp8_matmul("fp8_matmul_t", dY, w, ws, dX, lambda w: w.n_out, lambda w: w.k_in)
+    return _fp8_matmul("fp8_matmul_t", dY, w, ws, dX, True)
 
 
 @dataclass
@@ -788,11 +802,13 @@ class LoraLinear8:
     scale: float
 
     def c(self):
-        r = self.A.shape[1] if self.A.dim() == 2 else -1
+        A, B = self.A, self.B
         cw = self.w.c()
-        _t(self.A, "A", (self.w.k_in, r))
-        _t(self.B, "B", (r, self.w.n_out))
-        return QloraLoraLinear8(cw, self.A.data_ptr(), self.B.data_ptr(), r, self.scale)
+        n_out, k_in = self.w.codes.shape
+        r = A.shape[1] if A.dim() == 2 else -1
+        _t(A, "A", (k_in, r))
+        _t(B, "B", (r, n_out))
+        return QloraLoraLinear8(cw, A.data_ptr(), B.data_ptr(), r, self.scale)
 
 
 def qlora_linear8_workspace_bytes(M, K, N, r=16):
@@ -803,30 +819,29 @@ def qlora_linear8_fwd(lin: LoraLinear8, X, ws: Workspace, Y=None, XA=None, X8: F
     """Y = q(X) W^T + s (X A) B, XA = X A; X8 = X already in 8 bits (else the call quantises it)."""
     M = _rows(X)[0]
     c = lin.c()
-    n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
+    (k_in, r), n_out = lin.A.shape, lin.B.shape[1]
     _t(X, "X", (M, k_in))
     Y = X.new_empty((M, n_out)) if Y is None else _t(Y, "Y", (M, n_out))
     XA = X.new_empty((M, r)) if XA is None else _t(XA, "XA", (M, r))
     c8 = X8.c("X8", (M, k_in)) if X8 is not None else None
-    buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
-    _check("qlora_linear8_fwd", lib().qlora_linear8_fwd(ctypes.byref(c), _p(X), ctypes.byref(c8) if c8 else None, M,
-                                                        _p(Y), _p(XA), _p(buf), buf.numel(), _stream()))
+    _call_ws("qlora_linear8_fwd", ws, lambda: qlora_linear8_workspace_bytes(M, k_in, n_out, r),
+             (ctypes.byref(c), X.data_ptr(), ctypes.byref(c8) if c8 else None, M, Y.data_ptr(), XA.data_ptr()))
     return Y, XA
 
 
 def qlora_linear8_bwd(lin: LoraLinear8, X, XA, dY, ws: Workspace, dX=None, dA=None, dB=None):
     M = _rows(X)[0]
     c = lin.c()
-    n_out, k_in, r = lin.w.n_out, lin.w.k_in, lin.A.shape[1]
+    (k_in, r), n_out = lin.A.shape, lin.B.shape[1]
     _t(X, "X", (M, k_in))
     _t(XA, "XA", (M, r))
     _t(dY, "dY", (M, n_out))
     dX = X.new_empty((M, k_in)) if dX is None else _t(dX, "dX", (M, k_in))
     dA = X.new_empty((k_in, r)) if dA is None else _t(dA, "dA", (k_in, r))
     dB = X.new_empty((r, n_out)) if dB is None else _t(dB, "dB", (r, n_out))
-    buf = ws.get(qlora_linear8_workspace_bytes(M, k_in, n_out, r))
-    _check("qlora_linear8_bwd", lib().qlora_linear8_bwd(ctypes.byref(c), _p(X), _p(XA), _p(dY), M, _p(dX), _p(dA),
-                                                        _p(dB), _p(buf), buf.numel(), _stream()))
+    _call_ws("qlora_linear8_bwd", ws, lambda: qlora_linear8_workspace_bytes(M, k_in, n_out, r),
+             (ctypes.byref(c), X.data_ptr(), XA.data_ptr(), dY.data_ptr(), M, dX.data_ptr(), dA.data_ptr(),
+              dB.data_ptr()))
     return dX, dA, dB
 
 
