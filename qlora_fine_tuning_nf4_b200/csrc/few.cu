@@ -1,0 +1,358 @@
+// The passes of an e4m3 LoRA projection over T [M, C] (X forward, dY and X
+// backward) for a few rows, at most 64, each in one launch:
+//   forward   q(X), XA = X A
+//   backward  q(dY), G = dY B^T, dB = s XA^T dY     then     dA = X^T (s G)
+// Launches bound these sizes: the general path runs a quantiser, one or two passes
+// with fp32 partials and a reduction for each of them (9 launches a step, 5 here).
+//
+// T is taken in blocks of 128 columns, staged in shared memory together with the
+// low-rank factor's block (the next three blocks' copies are on their way meanwhile).
+// From there a block is quantised (fp8.cuh), multiplied into the low-rank sums and
+// used for the outer product, all with warp-level MMAs.  The blocks are dealt to
+// the CTAs of one cluster; its CTAs' low-rank sums meet through distributed shared
+// memory and are added in rank order, so nothing depends on timing.
+#include "fp8.cuh"
+
+namespace ql {
+
+constexpr int FW_ROWS = 64, FW_R = 64, FW_THREADS = 256;
+constexpr int FW_TP = 128 + 8;                 // row pitch of a staged block (elements): no bank conflicts
+constexpr int FW_T_BYTES = FW_ROWS * FW_TP * 2;
+constexpr int FW_V_BYTES = 128 * (FW_R + 8) * 2;  // [128][r + 8], or [r][128 + 8], whichever is larger
+static_assert(FW_V_BYTES >= FW_R * FW_TP * 2, "factor block");
+constexpr int FW_U_BYTES = FW_ROWS * (FW_R + 8) * 2;
+constexpr int FW_STAGES = 4;
+constexpr int FW_OFF_V = FW_STAGES * FW_T_BYTES, FW_OFF_U = FW_OFF_V + FW_STAGES * FW_V_BYTES;
+constexpr int FW_SMEM = FW_OFF_U + FW_U_BYTES;
+// Low-rank sums [row][FW_PP] of the four reduction shares, over the stages once they are done with.
+constexpr int FW_PP = FW_R + 8;
+constexpr int FW_PART = FW_ROWS * FW_PP;
+static_assert(4 * FW_PART * 4 <= FW_OFF_U, "the shares fit over the stages");
+
+enum FewMode : int { FEW_FWD = 0, FEW_BWD_DY = 1, FEW_BWD_DA = 2 };
+
+struct FewPass {
+  const bf16* T;     // [M, C]
+  int M, C, r;
+  uint8_t* codes;    // q(T): [M, C]; null: not wanted
+  float* tscale;     // [ceil(C / 128), M]
+  const bf16* V;     // low-rank factor: A [C, r] (forward) or B [r, C] (backward)
+  bf16 *low, *lows;  // T V and scale * T V as [M, r]; either may be null
+  const bf16* U;     // [M, r]: XA or s G
+  bf16* outer;       // dB [r, C] (scaled) or dA [C, r]
+  float scale;
+};
+
+QL_DEV void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+QL_DEV float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int mi = lane >> 3, mr = lane & 7;  // matrix and row that this lane addresses in an ldmatrix
+  const int mt = (a.M + 15) / 16;           // row tiles
+  const int nb = (a.C + 127) / 128;
+  const int first = blockIdx.x, step = gridDim.x;
+  const int r = a.r, lr = __ffs(r) - 1, lc = lr - 3;  // r is 16, 32 or 64: chunks of 8 by shifts
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // block kb of T (rows past M and columns past C as zeros) and of V into buffer b
+  auto stage = [&](int kb, int b) {
+    const int c0 = kb * 128;
+    for (int i = tid; i < mt * 16 * 16; i += FW_THREADS) {
+      const int m = i >> 4, c = (i & 15) * 8;
+      const bool in = m < a.M && c0 + c < a.C;
+      cp_async16(sb + b * FW_T_BYTES + (m * FW_TP + c) * 2,
+                 a.T + (in ? static_cast<size_t>(m) * a.C + c0 + c : 0), in);
+    }
+    const uint32_t v = sb + FW_OFF_V + b * FW_V_BYTES;
+    if constexpr (MODE == FEW_FWD) {  // [128][r + 8]
+      for (int i = tid; i < 128 << lc; i += FW_THREADS) {
+        const int k = i >> lc, c = (i - (k << lc)) * 8;
+        const bool in = c0 + k < a.C;
+        cp_async16(v + (k * (r + 8) + c) * 2, a.V + (in ? static_cast<size_t>(c0 + k) * r + c : 0), in);
+      }
+    } else if constexpr (MODE == FEW_BWD_DY) {  // [r][128 + 8]
+      for (int i = tid; i < r * 16; i += FW_THREADS) {
+        const int j = i >> 4, c = (i & 15) * 8;
+        const bool in = c0 + c < a.C;
+        cp_async16(v + (j * FW_TP + c) * 2, a.V + (in ? static_cast<size_t>(j) * a.C + c0 + c : 0), in);
+      }
+    }
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+  const uint32_t us = sb + FW_OFF_U;
+  if constexpr (MODE != FEW_FWD) {
+    for (int i = tid; i < (mt * 16) << lc; i += FW_THREADS) {
+      const int m = i >> lc, c = (i - (m << lc)) * 8;
+      cp_async16(us + (m * (r + 8) + c) * 2, a.U + (m < a.M ? static_cast<size_t>(m) * r + c : 0), m < a.M);
+    }
+  }
+  for (int s = 0; s < FW_STAGES - 1; ++s) {  // a group per stage, empty past the last block
+    if (first + s * step < nb) stage(first + s * step, s);
+    commit();
+  }
+
+  // low-rank sums: warps split a block's 8 reduction steps (two each, by warp & 3) and the factor's columns in two
+  const int kq = warp & 3, jh = warp >> 2, jt = r / 16;  // jt tiles of 8 columns per half
+  float acc[4][4][4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.f;
+
+  int b = 0;
+  for (int kb = first; kb < nb; kb += step, b = (b + 1) % FW_STAGES) {
+    const int ahead = kb + (FW_STAGES - 1) * step;
+    if (ahead < nb) stage(ahead, (b + FW_STAGES - 1) % FW_STAGES);
+    commit();
+    asm volatile("cp.async.wait_group %0;" ::"n"(FW_STAGES - 1) : "memory");  // this block's copies have landed
+    __syncthreads();
+    const uint32_t ts = sb + b * FW_T_BYTES, vs = sb + FW_OFF_V + b * FW_V_BYTES;
+
+    if constexpr (MODE != FEW_BWD_DA) {
+      // 8-bit rows (unless the caller has them): half a warp per row of the block
+      const int h = lane >> 4, c = (lane & 15) * 8, col = kb * 128 + c;
+      for (int m0 = warp * 2; a.codes && m0 < mt * 16; m0 += 16) {
+        const int m = m0 + h;
+        float f[8], s, inv;
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + b * FW_T_BYTES + (m * FW_TP + c) * 2), f);
+        fp8_scale(half_warp_max(absmax8(f)), s, inv);
+        if (m < a.M) {
+          if (col < a.C) *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * a.C + col) = e4m3x8(f, inv);
+          if (c == 0) a.tscale[static_cast<size_t>(kb) * a.M + m] = s;
+        }
+      }
+      // T V
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int k0 = (kq * 2 + s) * 16;
+        uint32_t bf[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          if (j >= jt) break;
+          const int n0 = (jh * jt + j) * 8;
+          if (jt == 1) {  // rank 16: one tile per half
+            if constexpr (MODE == FEW_FWD)
+              ldsm_x2_t(vs + ((k0 + (mi & 1) * 8 + mr) * (r + 8) + n0) * 2, bf[0][0], bf[0][1]);
+            else
+              ldsm_x2(vs + ((n0 + mr) * FW_TP + k0 + (mi & 1) * 8) * 2, bf[0][0], bf[0][1]);
+          } else {
+            if constexpr (MODE == FEW_FWD)
+              ldsm_x4_t(vs + ((k0 + (mi & 1) * 8 + mr) * (r + 8) + n0 + (mi >> 1) * 8) * 2, bf[j][0], bf[j][1],
+                        bf[j + 1][0], bf[j + 1][1]);
+            else
+              ldsm_x4(vs + ((n0 + (mi >> 1) * 8 + mr) * FW_TP + k0 + (mi & 1) * 8) * 2, bf[j][0], bf[j][1],
+                      bf[j + 1][0], bf[j + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (t >= mt) break;
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4(ts + ((t * 16 + (lane & 15)) * FW_TP + k0 + (lane >> 4) * 8) * 2, a0, a1, a2, a3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < jt) mma_bf16_16816(acc[t][j], a0, a1, a2, a3, bf[j][0], bf[j][1]);
+        }
+      }
+    }
+    const int g = lane >> 2, q = lane & 3;
+    if constexpr (MODE == FEW_BWD_DY) {
+      // dB = scale U^T T: r rows x this warp's 16 columns of the block, reduction over T's rows
+      float o[4][2][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][0][i] = o[j][1][i] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= mt) break;
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(ts + ((t * 16 + (mi & 1) * 8 + mr) * FW_TP + warp * 16 + (mi >> 1) * 8) * 2, b0, b1, b2, b3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j * 16 >= r) break;
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4_t(us + ((t * 16 + (mi >> 1) * 8 + mr) * (r + 8) + j * 16 + (mi & 1) * 8) * 2, a0, a1, a2, a3);
+          mma_bf16_16816(o[j][0], a0, a1, a2, a3, b0, b1);
+          mma_bf16_16816(o[j][1], a0, a1, a2, a3, b2, b3);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j * 16 >= r) break;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int col = kb * 128 + warp * 16 + n * 8 + q * 2;
+          if (col >= a.C) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint32_t*>(a.outer + static_cast<size_t>(j * 16 + h * 8 + g) * a.C + col) =
+                pack_bf16x2(o[j][n][2 * h] * a.scale, o[j][n][2 * h + 1] * a.scale);
+        }
+      }
+    }
+    if constexpr (MODE == FEW_BWD_DA) {
+      // dA = T^T U: this warp's 16 columns of the block x r
+      float o[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= mt) break;
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4_t(ts + ((t * 16 + (mi >> 1) * 8 + mr) * FW_TP + warp * 16 + (mi & 1) * 8) * 2, a0, a1, a2, a3);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          if (j * 8 >= r) break;
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(us + ((t * 16 + (mi & 1) * 8 + mr) * (r + 8) + j * 8 + (mi >> 1) * 8) * 2, b0, b1, b2, b3);
+          mma_bf16_16816(o[j], a0, a1, a2, a3, b0, b1);
+          mma_bf16_16816(o[j + 1], a0, a1, a2, a3, b2, b3);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j * 8 >= r) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = kb * 128 + warp * 16 + h * 8 + g;
+          if (n < a.C)
+            *reinterpret_cast<uint32_t*>(a.outer + static_cast<size_t>(n) * r + j * 8 + q * 2) =
+                pack_bf16x2(o[j][2 * h], o[j][2 * h + 1]);
+        }
+      }
+    }
+    __syncthreads();  // the buffer may be staged again
+  }
+
+  if constexpr (MODE != FEW_BWD_DA) {
+    float* part = reinterpret_cast<float*>(sm);
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t >= mt) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= jt) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(part + kq * FW_PART + (t * 16 + h * 8 + g) * FW_PP + (jh * jt + j) * 8 + q * 2) =
+              make_float2(acc[t][j][2 * h], acc[t][j][2 * h + 1]);
+      }
+    }
+    __syncthreads();
+    // this CTA's sum, in share 0
+    const int quads = a.M << (lr - 2);
+    for (int e = tid; e < quads; e += FW_THREADS) {
+      const int m = e >> (lr - 2), c = (e - (m << (lr - 2))) * 4;
+      float4* p = reinterpret_cast<float4*>(part + m * FW_PP + c);
+      float4 v = *p;
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(part + k * FW_PART + m * FW_PP + c);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      *p = v;
+    }
+    cluster_sync();
+    const int ranks = static_cast<int>(gridDim.x);  // the grid is one cluster
+    for (int e = tid + FW_THREADS * static_cast<int>(cluster_ctarank()); e < quads; e += FW_THREADS * ranks) {
+      const int m = e >> (lr - 2), c = (e - (m << (lr - 2))) * 4;
+      const uint32_t at = sb + (m * FW_PP + c) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = 0; c0 < ranks; c0 += 8) {  // eight ranks' loads in flight, added in rank order
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = c0 + i < ranks ? ld_cluster_f32x4(mapa_shared(at, static_cast<uint32_t>(c0 + i)))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.x += x[i].x, v.y += x[i].y, v.z += x[i].z, v.w += x[i].w;
+      }
+      const size_t o = static_cast<size_t>(m) * r + c;
+      if (a.low)
+        *reinterpret_cast<uint2*>(a.low + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (a.lows)
+        *reinterpret_cast<uint2*>(a.lows + o) =
+            make_uint2(pack_bf16x2(v.x * a.scale, v.y * a.scale), pack_bf16x2(v.z * a.scale, v.w * a.scale));
+    }
+    cluster_sync();  // no CTA leaves while another still reads its sums
+  }
+}
+
+template <int MODE>
+static cudaError_t launch_few_pass(const FewPass& a, cudaStream_t st) {
+  auto kern = few_pass_kernel<MODE>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(FW_THREADS);
+  cfg.dynamicSmemBytes = FW_SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  static int widest[64] = {0};  // CTAs of the widest cluster this device takes: 16 (opt-in) or 8
+  if (!widest[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FW_SMEM);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(16);
+    attr[0].val.clusterDim.x = 16;
+    const bool wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+    cudaGetLastError();
+    widest[dev] = wide ? 16 : 8;
+  }
+  const int nb = (a.C + 127) / 128;
+  int cluster = 1;
+  if (MODE != FEW_BWD_DA)  // the grid is one cluster
+    while (cluster * 2 <= nb && cluster * 2 <= widest[dev]) cluster *= 2;
+  attr[0].val.clusterDim.x = cluster;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(MODE == FEW_BWD_DA ? nb : cluster);
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// q(X) and XA (low), s XA (lows)
+cudaError_t launch_few_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
+                           bf16* low, bf16* lows, cudaStream_t st) {
+  return launch_few_pass<FEW_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale}, st);
+}
+// q(dY), s G (lows) and dB
+cudaError_t launch_few_bwd_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes,
+                              float* tscale, bf16* lows, const bf16* XA, bf16* dB, cudaStream_t st) {
+  return launch_few_pass<FEW_BWD_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale}, st);
+}
+// dA = X^T (s G)
+cudaError_t launch_few_bwd_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, cudaStream_t st) {
+  return launch_few_pass<FEW_BWD_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f}, st);
+}
+
+}  // namespace ql

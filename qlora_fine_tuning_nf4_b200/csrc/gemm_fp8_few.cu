@@ -19,8 +19,6 @@
 
 namespace ql {
 
-// Warps per CTA: 16 for up to 16 rows (128 registers a thread), 8 for up to 32.
-constexpr int few_warps(int mt) { return mt == 1 ? 16 : 8; }
 constexpr int FEW_COLS = 32;  // output columns per CTA
 
 // 4 x 4 bytes: word i holds row i; afterwards word j holds column j.
@@ -95,9 +93,9 @@ QL_DEV void few_load_x(const FewArgs& a, int kb, int m, int q, uint32_t (&v)[8])
   }
 }
 
-template <bool BWD, int MT>
-__global__ void __launch_bounds__(few_warps(MT) * 32, 1) gemm_fp8_few_kernel(const FewArgs a) {
-  constexpr int FEW_WARPS = few_warps(MT);
+// MT: row tiles of 16 (1 or 2).  FEW_WARPS: 16 or 8 per CTA.
+template <bool BWD, int MT, int FEW_WARPS>
+__global__ void __launch_bounds__(FEW_WARPS * 32, MT == 1 ? 16 / FEW_WARPS : 1) gemm_fp8_few_kernel(const FewArgs a) {
   extern __shared__ float part[];  // [warp][16 MT rows][32 columns]
   grid_dep_wait();
   grid_dep_launch();
@@ -180,21 +178,21 @@ __global__ void __launch_bounds__(few_warps(MT) * 32, 1) gemm_fp8_few_kernel(con
   }
 }
 
-template <bool BWD, int MT>
+template <bool BWD, int MT, int FEW_WARPS>
 static cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
-  constexpr int FEW_WARPS = few_warps(MT);
   constexpr int smem = FEW_WARPS * 16 * MT * FEW_COLS * 4;
   static_assert(smem <= 48 * 1024, "no opt-in needed");
-  return launch_pdl(gemm_fp8_few_kernel<BWD, MT>, dim3((a.cols + FEW_COLS - 1) / FEW_COLS), dim3(FEW_WARPS * 32), smem,
+  return launch_pdl(gemm_fp8_few_kernel<BWD, MT, FEW_WARPS>, dim3((a.cols + FEW_COLS - 1) / FEW_COLS), dim3(FEW_WARPS * 32), smem,
                     st, a);
 }
 
 cudaError_t launch_gemm_fp8_few(bool bwd, const uint8_t* x, const float* sa, const uint8_t* w, const float* sb,
                                 int sb_k, int sb_n, int M, int red, int cols, int ldw, const bf16* L, const bf16* R,
-                                int r, bf16* out, cudaStream_t st) {
+                                int r, bf16* out, int sms, cudaStream_t st) {
   const FewArgs a = {x, sa, w, sb, sb_k, sb_n, M, red, cols, ldw, L, R, r, out};
-  if (M <= 16) return bwd ? launch_few<true, 1>(a, st) : launch_few<false, 1>(a, st);
-  return bwd ? launch_few<true, 2>(a, st) : launch_few<false, 2>(a, st);
+  if (M > 16) return bwd ? launch_few<true, 2, 8>(a, st) : launch_few<false, 2, 8>(a, st);
+  if ((cols + FEW_COLS - 1) / FEW_COLS > sms) return bwd ? launch_few<true, 1, 8>(a, st) : launch_few<false, 1, 8>(a, st);
+  return bwd ? launch_few<true, 1, 16>(a, st) : launch_few<false, 1, 16>(a, st);
 }
 
 }  // namespace ql

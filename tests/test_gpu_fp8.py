@@ -175,7 +175,10 @@ def _linear(M, K, N, r, s, seed):
 
 LIN_SHAPES = [(1, 64, 16, 16, 1.0), (1, 1024, 528, 64, 0.25), (64, 4096, 1024, 64, 0.25), (130, 400, 272, 16, 2.0),
               (300, 512, 1040, 32, 0.5), (1030, 272, 384, 16, 1.0), (257, 1040, 2064, 64, 1.7),
-              (20, 512, 400, 32, 0.5), (33, 1680, 144, 16, 1.0), (90, 144, 1680, 64, 0.25), (2050, 1296, 1296, 32, 0.5)]
+              (20, 512, 400, 32, 0.5), (33, 1680, 144, 16, 1.0), (90, 144, 1680, 64, 0.25), (2050, 1296, 1296, 32, 0.5),
+              # the few-row passes' ends: 64 and 65 rows, one block of columns and more than a cluster's, each rank
+              (64, 272, 144, 32, 1.7), (65, 272, 144, 16, 0.5), (16, 4112, 2064, 64, 0.25), (48, 144, 6160, 16, 1.0),
+              (17, 128, 2064, 32, 1.0), (2, 16, 16, 64, 3.0)]
 
 
 @pytest.mark.parametrize("M,K,N,r,s", LIN_SHAPES)
