@@ -51,11 +51,11 @@ cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, in
 cudaError_t launch_gemm_fp8_few(bool bwd, const uint8_t* x, const float* sa, const uint8_t* w, const float* sb,
                                 int sb_k, int sb_n, int M, int red, int cols, int ldw, const bf16* L, const bf16* R,
                                 int r, bf16* out, int sms, cudaStream_t st);
-cudaError_t launch_few_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
-                           bf16* low, bf16* lows, cudaStream_t st);
-cudaError_t launch_few_bwd_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes,
-                              float* tscale, bf16* lows, const bf16* XA, bf16* dB, cudaStream_t st);
-cudaError_t launch_few_bwd_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, cudaStream_t st);
+cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
+                            bf16* low, bf16* lows, int sms, cudaStream_t st);
+cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
+                           bf16* lows, const bf16* XA, bf16* dB, int sms, cudaStream_t st);
+cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st);
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
                         int64_t ldo, cudaStream_t st);
@@ -71,13 +71,13 @@ namespace {
 enum KernelId : int {
   K_QUANT = 0, K_DEQUANT, K_GEMM_FWD, K_GEMM_GLU_FWD, K_GEMM_BWD, K_GEMM_GLU_BWD, K_ROWPROJ, K_COLPROJ, K_DYPASS,
   K_REDUCE, K_NORM_FWD, K_NORM_BWD, K_ADDNORM_FWD, K_ADDNORM_BWD, K_FP8_ROWS, K_FP8_QUANT, K_GEMM8_FWD, K_GEMM8_BWD,
-  K_GEMM8_SUM, K_FEW, K_ROPE, K_COUNT
+  K_GEMM8_SUM, K_PASS8, K_ROPE, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "gemm_nf4_fwd", "gemm_nf4_gateup_glu_fwd", "gemm_nf4_bwd_dx",
     "gemm_nf4_down_bwd_glu", "skinny_rowproj", "skinny_colproj", "skinny_dypass", "skinny_reduce", "rmsnorm_fwd", "rmsnorm_bwd",
     "add_rmsnorm_fwd", "add_rmsnorm_bwd", "fp8_quantize_rows", "fp8_quantize", "gemm_fp8_fwd", "gemm_fp8_bwd_dx",
-    "gemm_fp8_sum", "few_pass", "rope"};
+    "gemm_fp8_sum", "fp8_rank_pass", "rope"};
 
 std::atomic<uint64_t> g_launches{0};
 bool g_trace = false;
@@ -1558,8 +1558,11 @@ qlora_status fp8_matmul_t(const qlora_fp8_rows* dY, const qlora_fp8* w, int64_t 
 }
 
 namespace {
-// Rows up to which the passes around the products run in one launch each (few.cu).
-constexpr int64_t kFewRows = 64;
+// Rows up to which the passes around the products run in one launch each (fp8_passes.cu): the
+// backward's up to the 64 rows of one cluster; the forward's, a cluster per 64 rows, up to 256 rows, where
+// it saves two launches (128 rows, rank 64: 21.6 vs 23.7 us; 2048 rows, whose passes are bound by
+// bandwidth, 67.6 vs 49.3 us).
+constexpr int64_t kOnePassRows = 64, kFwdPassRows = 256;
 // Workspace of an e4m3 projection: [status word | 256 B][M x r vector][row codes][row scales][partials].
 // At ranks 32 and 64 the backward reduces its dB and dA passes in one launch at the end, so their
 // partials stay apart from those of the passes between: [dB][dA][the rest].
@@ -1618,14 +1621,15 @@ qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* 
   int* status = reinterpret_cast<int*>(w);
   const uint8_t* codes = X8 ? X8->codes : reinterpret_cast<uint8_t*>(w + l.codes);
   const float* scale = X8 ? X8->scale : reinterpret_cast<float*>(w + l.scale);
-  if (M <= kFewRows) {
+  if (M <= kFwdPassRows) {
     bf16* XAs = reinterpret_cast<bf16*>(w + l.vec);
     {
-      KScope k(K_FEW, st);
-      s = cuda_status(launch_few_fwd(reinterpret_cast<const bf16*>(X), (int)M, (int)K,
-                                     reinterpret_cast<const bf16*>(lin->A), r, lin->scale,
-                                     X8 ? nullptr : const_cast<uint8_t*>(codes), const_cast<float*>(scale),
-                                     reinterpret_cast<bf16*>(XA_saved), XAs, st));
+      KScope k(K_PASS8, st);
+      s = cuda_status(launch_pass_fwd(reinterpret_cast<const bf16*>(X), (int)M, (int)K,
+                                      reinterpret_cast<const bf16*>(lin->A), r, lin->scale,
+                                      X8 ? nullptr : reinterpret_cast<uint8_t*>(w + l.codes),
+                                      reinterpret_cast<float*>(w + l.scale), reinterpret_cast<bf16*>(XA_saved), XAs,
+                                      num_sms(), st));
     }
     if (s != QLORA_OK) return s;
     return gemm_fp8(false, codes, scale, lin->w, M, reinterpret_cast<bf16*>(Y), XAs,
@@ -1675,18 +1679,18 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
   const float sc = lin->scale;
   const bf16 *dy = reinterpret_cast<const bf16*>(dY), *x = reinterpret_cast<const bf16*>(X);
   const bf16* xa = reinterpret_cast<const bf16*>(XA_saved);
-  if (M <= kFewRows) {
+  if (M <= kOnePassRows) {
     {
-      KScope k(K_FEW, st);
-      s = cuda_status(launch_few_bwd_dy(dy, (int)M, (int)N, reinterpret_cast<const bf16*>(lin->B), r, sc, codes, scale,
-                                        sG, xa, reinterpret_cast<bf16*>(dB), st));
+      KScope k(K_PASS8, st);
+      s = cuda_status(launch_pass_dy(dy, (int)M, (int)N, reinterpret_cast<const bf16*>(lin->B), r, sc, codes, scale, sG,
+                                     xa, reinterpret_cast<bf16*>(dB), num_sms(), st));
     }
     if (s != QLORA_OK) return s;
     s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG,
                  reinterpret_cast<const bf16*>(lin->A), r, part, status, st);
     if (s != QLORA_OK) return s;
-    KScope k(K_FEW, st);
-    return cuda_status(launch_few_bwd_da(x, (int)M, (int)K, sG, r, reinterpret_cast<bf16*>(dA), st));
+    KScope k(K_PASS8, st);
+    return cuda_status(launch_pass_da(x, (int)M, (int)K, sG, r, reinterpret_cast<bf16*>(dA), num_sms(), st));
   }
   if ((s = fp8_quantize_rows(dY, M, N, codes, scale, stream)) != QLORA_OK) return s;
   const ReduceOuts gouts = routs(rout(sG, 0, r, r, 0, sc));

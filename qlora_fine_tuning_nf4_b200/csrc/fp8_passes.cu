@@ -1,16 +1,19 @@
-// The passes of an e4m3 LoRA projection over T [M, C] (X forward, dY and X
-// backward) for a few rows, at most 64, each in one launch:
-//   forward   q(X), XA = X A
-//   backward  q(dY), G = dY B^T, dB = s XA^T dY     then     dA = X^T (s G)
-// Launches bound these sizes: the general path runs a quantiser, one or two passes
-// with fp32 partials and a reduction for each of them (9 launches a step, 5 here).
+// The passes of an e4m3 LoRA projection around its products, over T [M, C]:
+//   forward   q(X), XA = X A                       (PASS_FWD, any M)
+//   backward  q(dY), G = dY B^T, dB = s XA^T dY    (PASS_DY, M <= 64)
+//             dA = X^T (s G)                       (PASS_DA, M <= 64)
+// each in one launch that reads T once, for the row counts that launches bound: the
+// general path runs a quantiser, one or two passes with fp32 partials and a reduction
+// for each of them (64 rows, rank 64, 4096 -> 1024: 12 launches a step, 44 us; here 6,
+// 33 us).
 //
-// T is taken in blocks of 128 columns, staged in shared memory together with the
-// low-rank factor's block (the next three blocks' copies are on their way meanwhile).
-// From there a block is quantised (fp8.cuh), multiplied into the low-rank sums and
-// used for the outer product, all with warp-level MMAs.  The blocks are dealt to
-// the CTAs of one cluster; its CTAs' low-rank sums meet through distributed shared
-// memory and are added in rank order, so nothing depends on timing.
+// A cluster takes 64 rows.  T comes in blocks of 128 columns, staged in shared
+// memory together with the low-rank factor's block (the next blocks' copies are on
+// their way meanwhile).  From there a block is quantised (fp8.cuh), multiplied into
+// the low-rank sums and used for the outer product, all with warp-level MMAs.  The
+// blocks are dealt to the cluster's CTAs, whose low-rank sums meet through
+// distributed shared memory and are added in rank order: no partials in memory, no
+// reduction launch, and nothing depends on timing.
 #include "fp8.cuh"
 
 namespace ql {
@@ -18,20 +21,25 @@ namespace ql {
 constexpr int FW_ROWS = 64, FW_R = 64, FW_THREADS = 256;
 constexpr int FW_TP = 128 + 8;                 // row pitch of a staged block (elements): no bank conflicts
 constexpr int FW_T_BYTES = FW_ROWS * FW_TP * 2;
-constexpr int FW_V_BYTES = 128 * (FW_R + 8) * 2;  // [128][r + 8], or [r][128 + 8], whichever is larger
-static_assert(FW_V_BYTES >= FW_R * FW_TP * 2, "factor block");
-constexpr int FW_U_BYTES = FW_ROWS * (FW_R + 8) * 2;
 constexpr int FW_STAGES = 4;
-constexpr int FW_OFF_V = FW_STAGES * FW_T_BYTES, FW_OFF_U = FW_OFF_V + FW_STAGES * FW_V_BYTES;
-constexpr int FW_SMEM = FW_OFF_U + FW_U_BYTES;
-// Low-rank sums [row][FW_PP] of the four reduction shares, over the stages once they are done with.
-constexpr int FW_PP = FW_R + 8;
-constexpr int FW_PART = FW_ROWS * FW_PP;
-static_assert(4 * FW_PART * 4 <= FW_OFF_U, "the shares fit over the stages");
+enum PassMode : int { PASS_FWD = 0, PASS_DY = 1, PASS_DA = 2 };
+// Bytes of a stage (a block of T and of the factor: [128][r + 8] forward, [r][128 + 8] backward), of U
+// [64][r + 8], and of the low-rank sums [64][r + 8] of the four reduction shares, which take the
+// stages' place once these are done with.
+__host__ __device__ constexpr int fw_stage_bytes(int mode, int r) {
+  return FW_T_BYTES + (mode == PASS_FWD ? 128 * (r + 8) * 2 : (mode == PASS_DA ? 0 : r * FW_TP * 2));
+}
+__host__ __device__ constexpr int fw_u_bytes(int mode, int r) {
+  return mode == PASS_FWD ? 0 : FW_ROWS * (r + 8) * 2;
+}
+__host__ __device__ constexpr int fw_smem(int mode, int r) {
+  return FW_STAGES * fw_stage_bytes(mode, r) + fw_u_bytes(mode, r);
+}
+static_assert(4 * FW_ROWS * (FW_R + 8) * 4 <= FW_STAGES * fw_stage_bytes(PASS_DY, FW_R) &&
+                  4 * FW_ROWS * (16 + 8) * 4 <= FW_STAGES * FW_T_BYTES && fw_smem(PASS_DY, FW_R) <= 232448,
+              "the shares fit over the stages, and everything into shared memory");
 
-enum FewMode : int { FEW_FWD = 0, FEW_BWD_DY = 1, FEW_BWD_DA = 2 };
-
-struct FewPass {
+struct RankPass {
   const bf16* T;     // [M, C]
   int M, C, r;
   uint8_t* codes;    // q(T): [M, C]; null: not wanted
@@ -41,6 +49,7 @@ struct FewPass {
   const bf16* U;     // [M, r]: XA or s G
   bf16* outer;       // dB [r, C] (scaled) or dA [C, r]
   float scale;
+  int cluster;       // CTAs per 64 rows
 };
 
 QL_DEV void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -56,15 +65,19 @@ QL_DEV float4 ld_cluster_f32x4(uint32_t addr) {
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
+__global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPass a) {
   extern __shared__ __align__(16) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int mi = lane >> 3, mr = lane & 7;  // matrix and row that this lane addresses in an ldmatrix
-  const int mt = (a.M + 15) / 16;           // row tiles
+  const int m0 = static_cast<int>(blockIdx.x / a.cluster) * FW_ROWS;  // the cluster's rows
+  const int M = min(FW_ROWS, a.M - m0);
+  const int mt = (M + 15) / 16;             // row tiles
   const int nb = (a.C + 127) / 128;
-  const int first = blockIdx.x, step = gridDim.x;
+  const int first = blockIdx.x % a.cluster, step = a.cluster;
   const int r = a.r, lr = __ffs(r) - 1, lc = lr - 3;  // r is 16, 32 or 64: chunks of 8 by shifts
+  const int stage_bytes = fw_stage_bytes(MODE, r);
+  const bf16* T = a.T + static_cast<size_t>(m0) * a.C;
   grid_dep_wait();
   grid_dep_launch();
 
@@ -73,18 +86,17 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
     const int c0 = kb * 128;
     for (int i = tid; i < mt * 16 * 16; i += FW_THREADS) {
       const int m = i >> 4, c = (i & 15) * 8;
-      const bool in = m < a.M && c0 + c < a.C;
-      cp_async16(sb + b * FW_T_BYTES + (m * FW_TP + c) * 2,
-                 a.T + (in ? static_cast<size_t>(m) * a.C + c0 + c : 0), in);
+      const bool in = m < M && c0 + c < a.C;
+      cp_async16(sb + b * stage_bytes + (m * FW_TP + c) * 2, T + (in ? static_cast<size_t>(m) * a.C + c0 + c : 0), in);
     }
-    const uint32_t v = sb + FW_OFF_V + b * FW_V_BYTES;
-    if constexpr (MODE == FEW_FWD) {  // [128][r + 8]
+    const uint32_t v = sb + b * stage_bytes + FW_T_BYTES;
+    if constexpr (MODE == PASS_FWD) {  // [128][r + 8]
       for (int i = tid; i < 128 << lc; i += FW_THREADS) {
         const int k = i >> lc, c = (i - (k << lc)) * 8;
         const bool in = c0 + k < a.C;
         cp_async16(v + (k * (r + 8) + c) * 2, a.V + (in ? static_cast<size_t>(c0 + k) * r + c : 0), in);
       }
-    } else if constexpr (MODE == FEW_BWD_DY) {  // [r][128 + 8]
+    } else if constexpr (MODE != PASS_DA) {  // [r][128 + 8]
       for (int i = tid; i < r * 16; i += FW_THREADS) {
         const int j = i >> 4, c = (i & 15) * 8;
         const bool in = c0 + c < a.C;
@@ -94,11 +106,11 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-  const uint32_t us = sb + FW_OFF_U;
-  if constexpr (MODE != FEW_FWD) {
+  const uint32_t us = sb + FW_STAGES * stage_bytes;
+  if constexpr (MODE != PASS_FWD) {
     for (int i = tid; i < (mt * 16) << lc; i += FW_THREADS) {
       const int m = i >> lc, c = (i - (m << lc)) * 8;
-      cp_async16(us + (m * (r + 8) + c) * 2, a.U + (m < a.M ? static_cast<size_t>(m) * r + c : 0), m < a.M);
+      cp_async16(us + (m * (r + 8) + c) * 2, a.U + (m < M ? static_cast<size_t>(m) * r + c : 0), m < M);
     }
   }
   for (int s = 0; s < FW_STAGES - 1; ++s) {  // a group per stage, empty past the last block
@@ -123,19 +135,19 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
     commit();
     asm volatile("cp.async.wait_group %0;" ::"n"(FW_STAGES - 1) : "memory");  // this block's copies have landed
     __syncthreads();
-    const uint32_t ts = sb + b * FW_T_BYTES, vs = sb + FW_OFF_V + b * FW_V_BYTES;
+    const uint32_t ts = sb + b * stage_bytes, vs = ts + FW_T_BYTES;
 
-    if constexpr (MODE != FEW_BWD_DA) {
+    if constexpr (MODE != PASS_DA) {
       // 8-bit rows (unless the caller has them): half a warp per row of the block
       const int h = lane >> 4, c = (lane & 15) * 8, col = kb * 128 + c;
-      for (int m0 = warp * 2; a.codes && m0 < mt * 16; m0 += 16) {
-        const int m = m0 + h;
+      for (int i = warp * 2; a.codes && i < mt * 16; i += 16) {
+        const int m = i + h;
         float f[8], s, inv;
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + b * FW_T_BYTES + (m * FW_TP + c) * 2), f);
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + b * stage_bytes + (m * FW_TP + c) * 2), f);
         fp8_scale(half_warp_max(absmax8(f)), s, inv);
-        if (m < a.M) {
-          if (col < a.C) *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * a.C + col) = e4m3x8(f, inv);
-          if (c == 0) a.tscale[static_cast<size_t>(kb) * a.M + m] = s;
+        if (m < M) {
+          if (col < a.C) *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m0 + m) * a.C + col) = e4m3x8(f, inv);
+          if (c == 0) a.tscale[static_cast<size_t>(kb) * a.M + m0 + m] = s;
         }
       }
       // T V
@@ -148,12 +160,12 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
           if (j >= jt) break;
           const int n0 = (jh * jt + j) * 8;
           if (jt == 1) {  // rank 16: one tile per half
-            if constexpr (MODE == FEW_FWD)
+            if constexpr (MODE == PASS_FWD)
               ldsm_x2_t(vs + ((k0 + (mi & 1) * 8 + mr) * (r + 8) + n0) * 2, bf[0][0], bf[0][1]);
             else
               ldsm_x2(vs + ((n0 + mr) * FW_TP + k0 + (mi & 1) * 8) * 2, bf[0][0], bf[0][1]);
           } else {
-            if constexpr (MODE == FEW_FWD)
+            if constexpr (MODE == PASS_FWD)
               ldsm_x4_t(vs + ((k0 + (mi & 1) * 8 + mr) * (r + 8) + n0 + (mi >> 1) * 8) * 2, bf[j][0], bf[j][1],
                         bf[j + 1][0], bf[j + 1][1]);
             else
@@ -173,7 +185,7 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
       }
     }
     const int g = lane >> 2, q = lane & 3;
-    if constexpr (MODE == FEW_BWD_DY) {
+    if constexpr (MODE == PASS_DY) {
       // dB = scale U^T T: r rows x this warp's 16 columns of the block, reduction over T's rows
       float o[4][2][4];
 #pragma unroll
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
         }
       }
     }
-    if constexpr (MODE == FEW_BWD_DA) {
+    if constexpr (MODE == PASS_DA) {
       // dA = T^T U: this warp's 16 columns of the block x r
       float o[8][4];
 #pragma unroll
@@ -244,8 +256,9 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
     __syncthreads();  // the buffer may be staged again
   }
 
-  if constexpr (MODE != FEW_BWD_DA) {
-    float* part = reinterpret_cast<float*>(sm);
+  if constexpr (MODE != PASS_DA) {
+    float* part = reinterpret_cast<float*>(sm);  // [share][row][pp]
+    const int pp = r + 8;
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -255,29 +268,29 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
         if (j >= jt) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(part + kq * FW_PART + (t * 16 + h * 8 + g) * FW_PP + (jh * jt + j) * 8 + q * 2) =
+          *reinterpret_cast<float2*>(part + kq * (FW_ROWS * pp) + (t * 16 + h * 8 + g) * pp + (jh * jt + j) * 8 + q * 2) =
               make_float2(acc[t][j][2 * h], acc[t][j][2 * h + 1]);
       }
     }
     __syncthreads();
     // this CTA's sum, in share 0
-    const int quads = a.M << (lr - 2);
+    const int quads = M << (lr - 2);
     for (int e = tid; e < quads; e += FW_THREADS) {
       const int m = e >> (lr - 2), c = (e - (m << (lr - 2))) * 4;
-      float4* p = reinterpret_cast<float4*>(part + m * FW_PP + c);
+      float4* p = reinterpret_cast<float4*>(part + m * pp + c);
       float4 v = *p;
 #pragma unroll
       for (int k = 1; k < 4; ++k) {
-        const float4 x = *reinterpret_cast<const float4*>(part + k * FW_PART + m * FW_PP + c);
+        const float4 x = *reinterpret_cast<const float4*>(part + k * (FW_ROWS * pp) + m * pp + c);
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
       *p = v;
     }
     cluster_sync();
-    const int ranks = static_cast<int>(gridDim.x);  // the grid is one cluster
-    for (int e = tid + FW_THREADS * static_cast<int>(cluster_ctarank()); e < quads; e += FW_THREADS * ranks) {
+    const int ranks = a.cluster;
+    for (int e = tid + FW_THREADS * first; e < quads; e += FW_THREADS * ranks) {
       const int m = e >> (lr - 2), c = (e - (m << (lr - 2))) * 4;
-      const uint32_t at = sb + (m * FW_PP + c) * 4;
+      const uint32_t at = sb + (m * pp + c) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int c0 = 0; c0 < ranks; c0 += 8) {  // eight ranks' loads in flight, added in rank order
         float4 x[8];
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v.x += x[i].x, v.y += x[i].y, v.z += x[i].z, v.w += x[i].w;
       }
-      const size_t o = static_cast<size_t>(m) * r + c;
+      const size_t o = static_cast<size_t>(m0 + m) * r + c;
       if (a.low)
         *reinterpret_cast<uint2*>(a.low + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       if (a.lows)
@@ -300,15 +313,14 @@ __global__ void __launch_bounds__(FW_THREADS) few_pass_kernel(const FewPass a) {
 }
 
 template <int MODE>
-static cudaError_t launch_few_pass(const FewPass& a, cudaStream_t st) {
-  auto kern = few_pass_kernel<MODE>;
+static cudaError_t launch_pass(RankPass a, int sms, cudaStream_t st) {
+  auto kern = fp8_rank_pass_kernel<MODE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(FW_THREADS);
-  cfg.dynamicSmemBytes = FW_SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -319,7 +331,8 @@ static cudaError_t launch_few_pass(const FewPass& a, cudaStream_t st) {
   cfg.attrs = attr;
   static int widest[64] = {0};  // CTAs of the widest cluster this device takes: 16 (opt-in) or 8
   if (!widest[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FW_SMEM);
+    cfg.dynamicSmemBytes = fw_smem(MODE, FW_R);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
     if (e != cudaSuccess) return e;
     int n = 0;
     cfg.numAttrs = 1;
@@ -330,29 +343,34 @@ static cudaError_t launch_few_pass(const FewPass& a, cudaStream_t st) {
     cudaGetLastError();
     widest[dev] = wide ? 16 : 8;
   }
-  const int nb = (a.C + 127) / 128;
-  int cluster = 1;
-  if (MODE != FEW_BWD_DA)  // the grid is one cluster
-    while (cluster * 2 <= nb && cluster * 2 <= widest[dev]) cluster *= 2;
-  attr[0].val.clusterDim.x = cluster;
+  // CTAs per 64 rows: enough to fill the device, at most one per block of columns
+  const int nb = (a.C + 127) / 128, groups = (a.M + FW_ROWS - 1) / FW_ROWS;
+  a.cluster = 1;
+  if (MODE == PASS_DA) a.cluster = nb;  // no sums to share: plain CTAs
+  else
+    while (a.cluster * 2 <= nb && a.cluster * 2 <= widest[dev] && groups * a.cluster < sms) a.cluster *= 2;
+  attr[0].val.clusterDim.x = MODE == PASS_DA ? 1 : a.cluster;
   cfg.numAttrs = 2;
-  cfg.gridDim = dim3(MODE == FEW_BWD_DA ? nb : cluster);
+  cfg.dynamicSmemBytes = fw_smem(MODE, a.r);
+  cfg.gridDim = dim3(static_cast<unsigned>(groups) * a.cluster);
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // q(X) and XA (low), s XA (lows)
-cudaError_t launch_few_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
-                           bf16* low, bf16* lows, cudaStream_t st) {
-  return launch_few_pass<FEW_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale}, st);
+cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
+                            bf16* low, bf16* lows, int sms, cudaStream_t st) {
+  return launch_pass<PASS_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale, 1}, sms, st);
 }
-// q(dY), s G (lows) and dB
-cudaError_t launch_few_bwd_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes,
-                              float* tscale, bf16* lows, const bf16* XA, bf16* dB, cudaStream_t st) {
-  return launch_few_pass<FEW_BWD_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale}, st);
+// q(dY), s G (lows) and dB = s XA^T dY, M <= 64
+cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
+                           bf16* lows, const bf16* XA, bf16* dB, int sms, cudaStream_t st) {
+  if (M > FW_ROWS) return cudaErrorInvalidValue;
+  return launch_pass<PASS_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale, 1}, sms, st);
 }
-// dA = X^T (s G)
-cudaError_t launch_few_bwd_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, cudaStream_t st) {
-  return launch_few_pass<FEW_BWD_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f}, st);
+// dA = X^T (s G), M <= 64
+cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st) {
+  if (M > FW_ROWS) return cudaErrorInvalidValue;
+  return launch_pass<PASS_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f, 1}, sms, st);
 }
 
 }  // namespace ql
