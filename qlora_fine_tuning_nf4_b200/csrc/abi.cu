@@ -48,9 +48,9 @@ cudaError_t launch_fp8_quantize(const bf16* w, int64_t N, int64_t K, uint8_t* co
 cudaError_t launch_gemm_fp8(bool bwd, int bn, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
 cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
                                 cudaStream_t st);
-cudaError_t launch_gemm_fp8_few(bool bwd, const uint8_t* x, const float* sa, const uint8_t* w, const float* sb,
-                                int sb_k, int sb_n, int M, int red, int cols, int ldw, const bf16* L, const bf16* R,
-                                int r, bf16* out, int sms, cudaStream_t st);
+cudaError_t launch_gemm_fp8_few(bool bwd, const CUtensorMap& map, const uint8_t* x, const float* sa, const float* sb,
+                                int sb_k, int sb_n, int M, int red, int cols, const bf16* L, const bf16* R, int r,
+                                bf16* out, int* status, cudaStream_t st);
 cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
                             bf16* low, bf16* lows, int sms, cudaStream_t st);
 cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
@@ -1483,16 +1483,20 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
   const int wkb = (int)cdiv(K, 128);  // the weight's scales are [ceil(n_out / 128), ceil(k_in / 128)]
   const int sb_k = bwd ? wkb : 1, sb_n = bwd ? 1 : wkb;
   const Fp8Plan plan = plan_fp8(M, red, out);
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (plan.few) {
+    CUtensorMap m;
+    if (!make_map(&m, u8, 1, w.codes, K, N, K, bwd ? 32 : 128, bwd ? 128 : 32,
+                  bwd ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+      return QLORA_ERR_CUDA;
     KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
-    return cuda_status(launch_gemm_fp8_few(bwd, codes, scale, w.codes, w.scale, sb_k, sb_n, (int)M, (int)red, (int)out,
-                                           (int)K, L, Rf, r, D, num_sms(), st));
+    return cuda_status(launch_gemm_fp8_few(bwd, m, codes, scale, w.scale, sb_k, sb_n, (int)M, (int)red, (int)out, L, Rf,
+                                           r, D, status, st));
   }
   const int bn = plan.bn;
   const int64_t prows = cdiv(M, 256) * 256;
   Gemm8Maps maps;
   std::memset(&maps, 0, sizeof(maps));
-  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!make_map(&maps.a, u8, 1, codes, red, M, red, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&maps.b, u8, 1, w.codes, K, N, K, bwd ? bn / 2 : 128, bwd ? 128 : bn / 2,
                 bwd && bn == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
