@@ -48,9 +48,10 @@ cudaError_t launch_fp8_quantize(const bf16* w, int64_t N, int64_t K, uint8_t* co
 cudaError_t launch_gemm_fp8(bool bwd, int bn, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
 cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
                                 cudaStream_t st);
-cudaError_t launch_gemm_fp8_few(bool bwd, const CUtensorMap& map, const uint8_t* x, const float* sa, const float* sb,
-                                int sb_k, int sb_n, int M, int red, int cols, const bf16* L, const bf16* R, int r,
-                                bf16* out, int* status, cudaStream_t st);
+int gemm_fp8_few_rows(int64_t M);
+cudaError_t launch_gemm_fp8_few(bool bwd, const FewMaps& maps, const float* sa, const float* sb, int sb_k, int sb_n,
+                                int M, int red, int cols, int cluster, int r, bf16* out, int* status,
+                                cudaStream_t st);
 cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
                             bf16* low, bf16* lows, int sms, cudaStream_t st);
 cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
@@ -1448,22 +1449,30 @@ qlora_status check_fp8(const qlora_fp8* w) {
 }
 // How a product of M rows, `red` reduction elements and `out` columns is run.
 struct Fp8Plan {
-  bool few;    // warp-level MMAs that stream the weight (gemm_fp8_few.cu)
-  int bn;      // columns per tile of the tcgen05 kernel
-  int splits;  // parts of its reduction
+  bool few;    // few rows: the weight is the MMA's row operand (gemm_fp8_few.cu)
+  int bn;      // else: columns per tile (gemm_fp8.cu)
+  int splits;  // parts of the reduction: CTAs of a cluster (few rows), or partial sums in the workspace
 };
 // Measured (us, one product; 4096 -> 4096 unless said otherwise):
-//  * few rows or tcgen05: 16 rows 5.7 vs 12.1; 32 rows 8.7 vs 11.4, but 28.4 vs 16.5 for 14336
-//    columns (more CTAs than SMs) and 32.9 vs 22.2 for a reduction of 14336 (long chains per warp);
+//  * few rows or tiles of 256: 16 rows 6.7 vs 12.6, 64 rows 8.5 vs 12.0 (from 65 rows on, the
+//    weight would be read once per 64 rows);
+//  * few rows, CTAs: one per SM, two where each keeps eight blocks or more: 4096 -> 11008 12.2 vs 11.0,
+//    but 1024 -> 4096 4.0 vs 4.3;
 //  * 128 or 256 columns per tile: 256 rows 12.4 vs 15.8 (32 or 16 tiles on 74 CTA pairs), 1024 rows
 //    22.2 vs 17.7;
-//  * parts of the reduction, where the tiles leave half the pairs idle: 256 rows, 14336 -> 4096 24.0 vs
-//    33.9; 128 rows, 4096 -> 1024 8.9 vs 12.2.  A part shorter than six blocks does not pay for the
-//    launch that adds the parts.
+//  * partial sums, where the tiles leave half the pairs idle: 256 rows, 14336 -> 4096 24.0 vs 33.9; 128
+//    rows, 4096 -> 1024 8.9 vs 12.2.  A part shorter than six blocks does not pay for the launch that
+//    adds the parts.
 Fp8Plan plan_fp8(int64_t M, int64_t red, int64_t out) {
   const int64_t sms = num_sms(), pairs = sms / 2, mt = cdiv(M, 256), nkb = cdiv(red, 128);
-  Fp8Plan p = {M <= 16 || (M <= 32 && cdiv(out, 32) <= sms && nkb <= 48), 256, 1};
-  if (p.few) return p;
+  Fp8Plan p = {M <= 64, 256, 1};
+  if (p.few) {
+    const int64_t tiles = cdiv(out, 128);
+    while (p.splits < 8 && p.splits * 2 <= nkb &&
+           (tiles * p.splits * 2 <= sms || (tiles * p.splits * 2 <= 2 * sms && nkb >= p.splits * 16)))
+      p.splits *= 2;
+    return p;
+  }
   if (mt * cdiv(out, 256) * 2 <= pairs) p.bn = 128;
   const int64_t tiles = mt * cdiv(out, p.bn);
   if (tiles * 2 <= pairs) p.splits = (int)std::max<int64_t>(1, std::min(pairs / tiles, nkb / 6));
@@ -1472,7 +1481,7 @@ Fp8Plan plan_fp8(int64_t M, int64_t red, int64_t out) {
 // fp32 partials of a split reduction
 size_t fp8_part_bytes(int64_t M, int64_t red, int64_t out) {
   const Fp8Plan p = plan_fp8(M, red, out);
-  return p.splits > 1 ? static_cast<size_t>(p.splits) * cdiv(M, 256) * 256 * out * 4 : 0;
+  return !p.few && p.splits > 1 ? static_cast<size_t>(p.splits) * cdiv(M, 256) * 256 * out * 4 : 0;
 }
 // D = x W^T (bwd = false) or x W, plus L Rt with the LoRA operands L [M, r] and B [r, n_out] or
 // A [k_in, r] (r = 0: none).  `part` has room for fp8_part_bytes.
@@ -1485,13 +1494,18 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
   const Fp8Plan plan = plan_fp8(M, red, out);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (plan.few) {
-    CUtensorMap m;
-    if (!make_map(&m, u8, 1, w.codes, K, N, K, bwd ? 32 : 128, bwd ? 128 : 32,
-                  bwd ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+    FewMaps m;
+    std::memset(&m, 0, sizeof(m));
+    const int nt = gemm_fp8_few_rows(M);
+    const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_map(&m.w, u8, 1, w.codes, K, N, K, 128, 128, swz) || !make_map(&m.x, u8, 1, codes, red, M, red, 128, nt, swz))
+      return QLORA_ERR_CUDA;
+    if (r > 0 && (!map_bf16(&m.l, L, r, M, r, 64, nt, swz) ||
+                  !(bwd ? map_bf16(&m.r, Rf, r, K, r, 64, 128, swz) : map_bf16(&m.r, Rf, N, r, N, 64, 64, swz))))
       return QLORA_ERR_CUDA;
     KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
-    return cuda_status(launch_gemm_fp8_few(bwd, m, codes, scale, w.scale, sb_k, sb_n, (int)M, (int)red, (int)out, L, Rf,
-                                           r, D, status, st));
+    return cuda_status(launch_gemm_fp8_few(bwd, m, scale, w.scale, sb_k, sb_n, (int)M, (int)red, (int)out, plan.splits, r,
+                                           D, status, st));
   }
   const int bn = plan.bn;
   const int64_t prows = cdiv(M, 256) * 256;

@@ -1,269 +1,328 @@
-// The block-scaled 8-bit product for a few rows (at most 32), with the LoRA term:
+// The block-scaled 8-bit product for a few rows (at most 64), with the LoRA term:
 //   Y = X W^T + (s X A) B  (BWD = false)  or  dX = dY W + (s dY B^T) A^T  (BWD = true)
 // with the operands and scales of gemm_fp8.cu.
 //
-// The weight's bytes bound it (each is read once), and with few rows the latency of
-// reading them: a CTA takes 32 output columns and all of the reduction, and one
-// thread streams the weight's blocks (32 x 128 bytes) by TMA into a 24-stage ring, so
-// two CTAs keep up to 192 KB per SM on their way.  Eight warps take the blocks in
-// turn.  Their fragments of warp-level MMAs (m16n8k32) need 4 consecutive reduction
-// elements per lane, but which ones is free as long as both operands agree, so lanes
-// read 16 bytes and call them two fragments.  For dX the reduction runs down the
-// columns of W: lane q of a quad reads words (4 columns) of the rows q, q + 4, ..., and
-// bytes are transposed 4 x 4 with byte permutes; the rows of dY, read as 32 bytes per
-// lane, are brought to the same order by a transpose across the quad.
+// The weight's bytes bound it: each is read once.  So the weight is the MMA's 128-row
+// operand and the few rows are its N (16, 32 or 64; rows past M are zeros from the
+// TMA): out^T = W X^T.  A cluster takes 128 output columns and its CTAs deal the
+// 128-wide reduction blocks among themselves, as many CTAs as fill the GPU.  Per CTA:
+//   warp 0       TMA producer: weight tiles (128 x 128 bytes) and the rows' blocks
+//   warp 1       TMEM allocation; issues tcgen05.mma, a fresh accumulator per block
+//   warp 2       scales: sa * sw of a block's rows into a shared-memory ring
+//   warps 4-7    accumulate: TMEM -> scale -> registers
+// Eight accumulators of 16 to 64 columns hide the way from the MMA to the accumulating
+// warps and back.  The CTAs' sums meet through distributed shared memory, are added in
+// rank order and leave as bf16.  The LoRA term is one more block of the last CTA: bf16
+// operands (kind::f16) and scale 1.
 //
-// Each block's product is formed in fp32 from zero, scaled and added to the warp's
-// sums; the warps' sums meet in shared memory and are added in warp order.
-//
-// With weights that come from HBM: 16 rows, 4096 -> 4096 FWD_US us, 4096 -> 14336 (59 MB, 9.1 us at
-// the copy rate) BIG_US us.
+// With weights that come from HBM: one row, 4096 -> 14336 (59 MB, 9.1 us at the copy
+// rate) 12.9 us, 4096 -> 4096 (17 MB, 2.6 us) 6.5 us; 64 rows 16.2 and 8.5 us.  Warp-level
+// MMAs fed by the same ring of TMA loads took 17.5 us for the former: an e4m3
+// m16n8k32 occupies a scheduler for about 64 cycles, so they were bound by it.  Stages
+// for two CTAs per SM rather than one: the next CTA (or the next launch's) sets up
+// while this one drains (64 rows, 4096 -> 4096: 12.1 -> 8.5 us).
 #include "kernels.cuh"
 #include "ptx.cuh"
 
 namespace ql {
 
-constexpr int FEW_WARPS = 8;                      // consumer warps; one more streams the weight
-constexpr int FEW_THREADS = (FEW_WARPS + 1) * 32;
-constexpr int FEW_COLS = 32;                      // output columns per CTA
-constexpr int FEW_STAGES = 24;
-constexpr int FEW_BLOCK = FEW_COLS * 128;         // bytes of a weight block
-constexpr int FEW_OFF_BAR = FEW_STAGES * FEW_BLOCK;
-constexpr int FEW_SMEM = FEW_OFF_BAR + 2 * FEW_STAGES * 8 + 1024;  // + alignment slack
-// The warps' sums [warp][16 MT rows][32 columns] take the ring's place at the end.
-static_assert(FEW_WARPS * 32 * FEW_COLS * 4 <= FEW_OFF_BAR, "the sums fit over the ring");
-
-// 4 x 4 bytes: word i holds row i; afterwards word j holds column j.
-QL_DEV void transpose4x4(uint32_t& w0, uint32_t& w1, uint32_t& w2, uint32_t& w3) {
-  const uint32_t a = prmt(w0, w1, 0x5140u), b = prmt(w0, w1, 0x7362u);  // r0c0 r1c0 r0c1 r1c1 | c2, c3
-  const uint32_t c = prmt(w2, w3, 0x5140u), d = prmt(w2, w3, 0x7362u);
-  w0 = prmt(a, c, 0x5410u);
-  w1 = prmt(a, c, 0x7632u);
-  w2 = prmt(b, d, 0x5410u);
-  w3 = prmt(b, d, 0x7632u);
-}
-// Across a quad of lanes: lane q's word s becomes lane s's word q.
-QL_DEV void quad_transpose(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, int q) {
-  auto swap = [q](uint32_t& lo, uint32_t& hi, int bit) {
-    const bool up = (q & bit) != 0;
-    const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
-    if (up) lo = y;
-    else hi = y;
-  };
-  swap(r0, r1, 1);
-  swap(r2, r3, 1);
-  swap(r0, r2, 2);
-  swap(r1, r3, 2);
-}
+template <int NT>
+struct FewCfg {
+  static constexpr int BM = 128;                 // output columns per cluster (the MMA's rows)
+  static constexpr int W_BYTES = BM * 128;       // a block of the weight
+  static constexpr int X_BYTES = NT * 128;       // a block of the rows
+  static constexpr int S = NT == 64 ? 4 : 5;     // operand stages: two CTAs fit on an SM
+  static constexpr int ACCS = NT == 64 ? 4 : 8;
+  static constexpr int SR = S + ACCS + 2;        // scale slots (as in gemm_fp8.cu)
+  static constexpr int G = 8;                    // blocks whose scales are requested together
+  static constexpr int OFF_X = S * W_BYTES;
+  static constexpr int OFF_SC = OFF_X + S * X_BYTES;
+  static constexpr int OFF_BAR = OFF_SC + SR * NT * 4;
+  static constexpr int NBAR = 2 * S + 2 * ACCS + 1;
+  static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int THREADS = 256;
+  static constexpr int TMEM_COLS = ACCS * NT;
+  static_assert(SMEM_BYTES <= 232448 / 2 - 1024 && 2 * TMEM_COLS <= 512, "two CTAs per SM");
+  static_assert(NT * BM * 4 <= S * W_BYTES, "a CTA's sums fit over the stages");
+};
 
 struct FewArgs {
-  const uint8_t* x;   // e4m3 [M, red]
   const float* sa;    // [blocks, M]
   const float* sb;    // weight scales, strides per reduction block and per 128 output columns
   int sb_k, sb_n;
-  int M, red, cols;   // rows, reduction length, output columns
-  const bf16 *L, *R;  // LoRA operands: L [M, r]; R = B [r, n_out] or A [k_in, r]
-  int r;              // 0: no adapter
+  int M, nkb, cols;   // rows, reduction blocks, output columns
+  int cluster;        // CTAs that share a tile's reduction
+  int lora_k16;       // 16-wide reduction steps of the LoRA operands (rank / 16), 0 = no adapter
   bf16* out;          // [M, cols]
   int* status;
 };
 
-// The lane's 32 bytes of row m in block kb.
-template <bool BWD>
-QL_DEV void few_load_x(const FewArgs& a, int kb, int m, int q, uint32_t (&v)[8]) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int k = kb * 128 + (BWD ? q * 32 + c * 16 : c * 64 + q * 16);
-    const uint4 u = m < a.M && k < a.red
-                        ? __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(m) * a.red + k))
-                        : make_uint4(0, 0, 0, 0);
-    v[c * 4] = u.x;
-    v[c * 4 + 1] = u.y;
-    v[c * 4 + 2] = u.z;
-    v[c * 4 + 3] = u.w;
-  }
+QL_DEV float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
-// MT: row tiles of 16 (1 or 2).  map: e4m3 weight [n_out, k_in], box {128, 32} with 128B swizzle
-// (forward) or {32, 128} (dX).
-template <bool BWD, int MT>
-__global__ void __launch_bounds__(FEW_THREADS, MT == 1 ? 2 : 1)
-    gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap map, const FewArgs a) {
+template <bool BWD, int NT>
+__global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
+    gemm_fp8_few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+  using C = FewCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * FEW_COLS;
-  const int nkb = (a.red + 127) / 128;
-  auto full_bar = [&](int s) { return sbase + FEW_OFF_BAR + 8u * s; };
-  auto empty_bar = [&](int s) { return sbase + FEW_OFF_BAR + 8u * (FEW_STAGES + s); };
+  const int rank = static_cast<int>(blockIdx.x % a.cluster);
+  const int n0 = static_cast<int>(blockIdx.x / a.cluster) * C::BM;
+  const int own = (a.nkb - rank + a.cluster - 1) / a.cluster;  // blocks rank, rank + cluster, ...
+  const int mine = own + (a.lora_k16 > 0 && rank == a.cluster - 1 ? 1 : 0);
+
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::S + s); };
+  const uint32_t acc_full0 = bar0 + 8u * (2 * C::S);
+  const uint32_t acc_empty0 = acc_full0 + 8u * C::ACCS;
+  const uint32_t drain_bar = acc_empty0 + 8u * C::ACCS;
+  float* const scales = reinterpret_cast<float*>(sgen + C::OFF_SC);  // [slot][row]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sgen + C::OFF_BAR + C::NBAR * 8);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < FEW_STAGES; ++s) {
-      mbar_init(full_bar(s), 1);
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(full_bar(s), 2);  // the loads, and the scales
       mbar_init(empty_bar(s), 1);
     }
+    for (int b = 0; b < C::ACCS; ++b) {
+      mbar_init(acc_full0 + 8u * b, 1);
+      mbar_init(acc_empty0 + 8u * b, 4);
+    }
+    mbar_init(drain_bar, 1);
     fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(tmem_holder), C::TMEM_COLS);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   grid_dep_wait();
   grid_dep_launch();
-  float acc[MT][4][4];
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.f;
-  const int g = lane >> 2, q = lane & 3;
-  if (warp == FEW_WARPS) {
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
     bool ok = true;
-    for (int kb = 0; kb < nkb && ok; ++kb) {
-      const int s = kb % FEW_STAGES;
-      ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ((kb / FEW_STAGES) & 1) ^ 1, a.status));
+    int s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < mine; ++i) {
+      const int kb = rank + i * a.cluster;
+      ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, a.status));
       if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(full_bar(s), FEW_BLOCK);
-        if (BWD) tma_load_2d(sbase + s * FEW_BLOCK, &map, full_bar(s), n0, kb * 128);
-        else tma_load_2d(sbase + s * FEW_BLOCK, &map, full_bar(s), kb * 128, n0);
+        mbar_arrive_expect_tx(full_bar(s), C::W_BYTES + C::X_BYTES);
+        const uint32_t w = sbase + s * C::W_BYTES, x = sbase + C::OFF_X + s * C::X_BYTES;
+        if (i < own) {
+          // W rows x reduction bytes (K-major), or reduction rows x output columns (MN-major)
+          if (BWD) tma_load_2d(w, &maps.w, full_bar(s), n0, kb * 128);
+          else tma_load_2d(w, &maps.w, full_bar(s), kb * 128, n0);
+          tma_load_2d(x, &maps.x, full_bar(s), kb * 128, 0);
+        } else {
+          // LoRA operands, 64 wide with zeros beyond the rank: A [128 columns, r] K-major (dX), or
+          // B [r, 128 columns] MN-major in chunks of 64 columns (forward)
+          if (BWD) {
+            tma_load_2d(w, &maps.r, full_bar(s), 0, n0);
+          } else {
+            tma_load_2d(w, &maps.r, full_bar(s), n0, 0);
+            tma_load_2d(w + 8192, &maps.r, full_bar(s), n0 + 64, 0);
+          }
+          tma_load_2d(x, &maps.l, full_bar(s), 0, 0);
+        }
       }
       __syncwarp();
+      if (++s == C::S) s = 0, ph ^= 1;
     }
     if (!ok) settle_inflight();  // loads already issued land before the CTA can exit
-  } else {
-    const float* sb = a.sb + static_cast<size_t>(n0 / 128) * a.sb_n;  // 32 columns lie in one block of 128
-    uint32_t xn[MT][2][8];  // one block ahead
-    float scn[MT][2], swn = 0.f;
-    auto request = [&](int kb) {
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA -----
+    bool ok = true;
+    constexpr uint32_t idesc = idesc_e4m3(C::BM, NT, BWD, false);
+    constexpr uint32_t idesc_lora = idesc_bf16(C::BM, NT, !BWD, false);
+    const uint64_t wd0 = smem_desc(sbase, BWD ? C::W_BYTES : 16, 1024, QL_SWZ_128B);
+    const uint64_t xd0 = smem_desc(sbase + C::OFF_X, 16, 1024, QL_SWZ_128B);
+    const uint64_t rd0 = smem_desc(sbase, BWD ? 16 : 8192, 1024, QL_SWZ_128B);
+    int s = 0, b = 0;
+    uint32_t ph = 0, aph = 1;
+    for (int i = 0; i < mine; ++i) {
+      ok = mbar_wait(full_bar(s), ph, a.status) && mbar_wait(acc_empty0 + 8u * b, aph, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t wo = static_cast<uint64_t>(s) * (C::W_BYTES >> 4);
+        const uint64_t xd = xd0 + static_cast<uint64_t>(s) * (C::X_BYTES >> 4);
+        if (i < own) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int m = t * 16 + h * 8 + g;
-          few_load_x<BWD>(a, kb, m, q, xn[t][h]);
-          scn[t][h] = m < a.M ? __ldg(a.sa + static_cast<size_t>(kb) * a.M + m) : 0.f;
+          for (int kk = 0; kk < 4; ++kk)  // 32 reduction elements each
+            umma_e4m3<1>(tmem + b * NT, wd0 + wo + kk * (BWD ? 256 : 2), xd + kk * 2, idesc, kk != 0);
+        } else {
+          for (int kk = 0; kk < a.lora_k16; ++kk)
+            umma_bf16<1>(tmem + b * NT, rd0 + wo + kk * (BWD ? 2 : 128), xd + kk * 2, idesc_lora, kk != 0);
         }
-      swn = __ldg(sb + static_cast<size_t>(kb) * a.sb_k);
-    };
-    if (warp < nkb) request(warp);
-    for (int kb = warp; kb < nkb; kb += FEW_WARPS) {
-      uint32_t w[32], x[MT][2][8];
-      float sc[MT][2];
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[t][h][i] = xn[t][h][i];
-          sc[t][h] = scn[t][h] * swn;
-          if constexpr (BWD) {
-            // bytes of the lane's 32 consecutive elements -> bytes q, q + 4, q + 8, q + 12 of every 16
-            transpose4x4(x[t][h][0], x[t][h][1], x[t][h][2], x[t][h][3]);
-            transpose4x4(x[t][h][4], x[t][h][5], x[t][h][6], x[t][h][7]);
-            quad_transpose(x[t][h][0], x[t][h][1], x[t][h][2], x[t][h][3], q);
-            quad_transpose(x[t][h][4], x[t][h][5], x[t][h][6], x[t][h][7], q);
-          }
-        }
-      if (kb + FEW_WARPS < nkb) request(kb + FEW_WARPS);
-      const int s = kb % FEW_STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait(full_bar(s), (kb / FEW_STAGES) & 1, a.status))) break;
-      const uint8_t* blk = sgen + s * FEW_BLOCK;
-      if constexpr (!BWD) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint4 u = *reinterpret_cast<const uint4*>(blk + (j * 8 + g) * 128 + (((c * 4 + q) ^ g) << 4));
-            w[j * 8 + c * 4] = u.x;
-            w[j * 8 + c * 4 + 1] = u.y;
-            w[j * 8 + c * 4 + 2] = u.z;
-            w[j * 8 + c * 4 + 3] = u.w;
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = *reinterpret_cast<const uint32_t*>(blk + (i * 4 + q) * 32 + g * 4);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) transpose4x4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        umma_commit<1>(empty_bar(s));
+        umma_commit<1>(acc_full0 + 8u * b);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float tmp[MT][4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmp[t][i] = 0.f;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {  // 32 reduction elements each
-          const uint32_t b0 = BWD ? w[p * 8 + j] : w[j * 8 + 2 * p];
-          const uint32_t b1 = BWD ? w[p * 8 + 4 + j] : w[j * 8 + 2 * p + 1];
-          constexpr int kLo = BWD ? 1 : 2, kHi = BWD ? 4 : 1;  // word of step p, and the distance to its second
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            mma_e4m3_16832(tmp[t], x[t][0][kLo * p], x[t][1][kLo * p], x[t][0][kLo * p + kHi], x[t][1][kLo * p + kHi],
-                           b0, b1);
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(tmp[t][i], sc[t][i >> 1], acc[t][j][i]);
-      }
-      // Released once the products have consumed what was read from it (an arrive right after the
-      // loads could overtake them).
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(s));
+      if (++s == C::S) s = 0, ph ^= 1;
+      if (++b == C::ACCS) b = 0, aph ^= 1;
+    }
+    // let every issued MMA finish before TMEM can be released (after an error too)
+    if (elect_one()) umma_commit<1>(drain_bar);
+    __syncwarp();
+    mbar_drain(drain_bar, 0);
+  } else if (warp == 2) {
+    // ------------------------------------------------------ scales -----
+    bool ok = true;
+    int s = 0, sl = 0;
+    uint32_t ph = 1;
+    const float* sb = a.sb + static_cast<size_t>(n0 / 128) * a.sb_n;
+    for (int i0 = 0; i0 < mine && ok; i0 += C::G) {
+      float v[C::G][NT / 32 + (NT < 32)];
+#pragma unroll
+      for (int g = 0; g < C::G; ++g) {
+        const int kb = rank + (i0 + g) * a.cluster;
+        const float lora = i0 + g == own ? 1.f : 0.f;
+        const float w = kb < a.nkb ? __ldg(sb + static_cast<size_t>(kb) * a.sb_k) : 0.f;
+#pragma unroll
+        for (int h = 0; h < NT / 32 + (NT < 32); ++h) {
+          const int m = h * 32 + lane;
+          v[g][h] = kb < a.nkb && m < a.M ? w * __ldg(a.sa + static_cast<size_t>(kb) * a.M + m) : lora;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < C::G; ++g) {
+        if (i0 + g >= mine) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph, a.status));
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < NT / 32 + (NT < 32); ++h)
+          if (h * 32 + lane < NT) scales[sl * NT + h * 32 + lane] = v[g][h];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(s));
+        if (++s == C::S) s = 0, ph ^= 1;
+        if (++sl == C::SR) sl = 0;
+      }
     }
   }
-  __syncthreads();  // every block has been used: the sums may take the ring's place
-  float* part = reinterpret_cast<float*>(sgen);
-  if (warp < FEW_WARPS) {
-    // columns of the fragments: group j is columns 8 j .. 8 j + 7 (forward), or j, j + 4, ... (dX)
+  float acc[NT];
+  if (warp >= 4) {
+    // ------------------------------------------------------ accumulate ---
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+    const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int b = 0, sl = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < mine; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8u * b, ph, a.status))) break;
+      tc_fence_after();
+      const float4* sc = reinterpret_cast<const float4*>(scales + sl * NT);
+      if (++sl == C::SR) sl = 0;
+      constexpr int CH = NT < 32 ? NT : 32;  // columns loaded at a time
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int c0 = 0; c0 < NT; c0 += CH) {
+        uint32_t v[CH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 2 * q + (i & 1), m = t * 16 + (i >> 1) * 8 + g;
-          part[(warp * 16 * MT + m) * FEW_COLS + (BWD ? c * 4 + j : j * 8 + c)] = acc[t][j][i];
+        for (int c = 0; c < CH; c += 16) tmem_ld_32x32b_x16_async(tmem + quad + b * NT + c0 + c, v + c);
+#pragma unroll
+        for (int c = 0; c < CH; c += 16) tmem_wait_ld16(v + c);
+#pragma unroll
+        for (int c = 0; c < CH; c += 4) {
+          const float4 x = sc[(c0 + c) / 4];
+          acc[c0 + c] = fmaf(__uint_as_float(v[c]), x.x, acc[c0 + c]);
+          acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), x.y, acc[c0 + c + 1]);
+          acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), x.z, acc[c0 + c + 2]);
+          acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), x.w, acc[c0 + c + 3]);
         }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty0 + 8u * b);
+      if (++b == C::ACCS) b = 0, ph ^= 1;
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * MT * FEW_COLS; i += FEW_THREADS) {
-    const int m = i / FEW_COLS, n = n0 + i % FEW_COLS;
-    if (m >= a.M) break;
-    if (n >= a.cols) continue;
-    float v = 0.f;
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();  // every block has been added: the sums may take the stages' place
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, C::TMEM_COLS);
+  }
+  float* red = reinterpret_cast<float*>(sgen);  // [row][128 columns]
+  if (warp >= 4) {
 #pragma unroll
-    for (int k = 0; k < FEW_WARPS; ++k) v += part[k * 16 * MT * FEW_COLS + i];
-    for (int k = 0; k < a.r; ++k)
-      v = fmaf(__bfloat162float(a.L[static_cast<size_t>(m) * a.r + k]),
-               __bfloat162float(BWD ? a.R[static_cast<size_t>(n) * a.r + k] : a.R[static_cast<size_t>(k) * a.cols + n]), v);
-    a.out[static_cast<size_t>(m) * a.cols + n] = __float2bfloat16(v);
+    for (int i = 0; i < NT; ++i) red[i * C::BM + (warp & 3) * 32 + lane] = acc[i];
   }
+  cluster_sync();
+  // each CTA finishes every cluster-th row, four columns per thread (cols % 16 == 0)
+  for (int i = threadIdx.x; i < (a.M - rank + a.cluster - 1) / a.cluster * (C::BM / 4); i += C::THREADS) {
+    const int m = rank + i / (C::BM / 4) * a.cluster, c = i % (C::BM / 4) * 4, n = n0 + c;
+    if (n >= a.cols) continue;
+    float4 x[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (p < a.cluster) x[p] = ld_cluster_f32x4(mapa_shared(sbase + (m * C::BM + c) * 4, static_cast<uint32_t>(p)));
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (p < a.cluster) v[0] += x[p].x, v[1] += x[p].y, v[2] += x[p].z, v[3] += x[p].w;
+    *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(m) * a.cols + n) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
-template <bool BWD, int MT>
-static cudaError_t launch_few(const CUtensorMap& map, const FewArgs& a, cudaStream_t st) {
-  auto kern = gemm_fp8_few_kernel<BWD, MT>;
+template <bool BWD, int NT>
+static cudaError_t launch_few(const FewMaps& maps, const FewArgs& a, cudaStream_t st) {
+  using C = FewCfg<NT>;
+  auto kern = gemm_fp8_few_kernel<BWD, NT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static bool set[64] = {false};
   if (!set[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  return launch_pdl(kern, dim3((a.cols + FEW_COLS - 1) / FEW_COLS), dim3(FEW_THREADS), FEW_SMEM, st, map, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.cols + C::BM - 1) / C::BM * a.cluster));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
-cudaError_t launch_gemm_fp8_few(bool bwd, const CUtensorMap& map, const uint8_t* x, const float* sa, const float* sb,
-                                int sb_k, int sb_n, int M, int red, int cols, const bf16* L, const bf16* R, int r,
-                                bf16* out, int* status, cudaStream_t st) {
-  const FewArgs a = {x, sa, sb, sb_k, sb_n, M, red, cols, L, R, r, out, status};
-  if (M > 32) return cudaErrorInvalidValue;
-  if (M > 16) return bwd ? launch_few<true, 2>(map, a, st) : launch_few<false, 2>(map, a, st);
-  return bwd ? launch_few<true, 1>(map, a, st) : launch_few<false, 1>(map, a, st);
+// Rows per MMA (the box of the rows' tensor map): M rounded up to 16, 32 or 64.
+int gemm_fp8_few_rows(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
+
+cudaError_t launch_gemm_fp8_few(bool bwd, const FewMaps& maps, const float* sa, const float* sb, int sb_k, int sb_n,
+                                int M, int red, int cols, int cluster, int r, bf16* out, int* status,
+                                cudaStream_t st) {
+  const FewArgs a = {sa, sb, sb_k, sb_n, M, (red + 127) / 128, cols, cluster, r / 16, out, status};
+  if (M > 64) return cudaErrorInvalidValue;
+  if (M > 32) return bwd ? launch_few<true, 64>(maps, a, st) : launch_few<false, 64>(maps, a, st);
+  if (M > 16) return bwd ? launch_few<true, 32>(maps, a, st) : launch_few<false, 32>(maps, a, st);
+  return bwd ? launch_few<true, 16>(maps, a, st) : launch_few<false, 16>(maps, a, st);
 }
 
 }  // namespace ql

@@ -90,6 +90,15 @@ struct Gemm8Args {
   int prows;            // rows of a part's partials (M rounded up to whole tiles)
 };
 
+// The same product for few rows: the weight is the 128-row operand of the MMA and NT = 16, 32 or 64
+// rows its columns.
+struct FewMaps {
+  CUtensorMap w;  // weight: e4m3 [n_out, k_in], box {128, 128}, 128B swizzle (all four)
+  CUtensorMap x;  // rows: e4m3 [M, reduction], box {128, NT}
+  CUtensorMap l;  // LoRA left operand: bf16 [M, r], box {64, NT}
+  CUtensorMap r;  // LoRA right operand: B [r, n_out], box {64, 64} (forward), or A [k_in, r], box {64, 128} (dX)
+};
+
 // --------------------------------------------------------------- skinny ---
 // Rank-r products on warp-level mma.sync.  Each skinny kernel is persistent:
 // its P CTAs split the work units (64 x 64 tiles, or 64-row x 256-column

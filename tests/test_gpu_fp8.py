@@ -91,7 +91,7 @@ def _values(x, sx, w, sw):
 MM_SHAPES = [(1, 64, 16), (1, 4096, 4096), (3, 16, 16), (16, 1024, 512), (17, 144, 272), (64, 512, 128), (128, 256, 384),
              (130, 1040, 528), (200, 2048, 144), (256, 128, 256), (257, 400, 2064), (520, 384, 1552), (1025, 272, 640),
              # 17 to 32 rows; parts of a long reduction, in both directions; tiles of 256 columns, in both directions
-             (20, 528, 400), (32, 2048, 1040), (70, 4096, 80), (130, 144, 2064), (300, 80, 6160), (33, 1552, 16),
+             (20, 528, 400), (32, 2048, 1040), (33, 2048, 528), (64, 1552, 2064), (5, 14336, 144), (64, 16, 4112), (70, 4096, 80), (130, 144, 2064), (300, 80, 6160), (33, 1552, 16),
              (2050, 272, 1296), (2050, 1296, 272), (1300, 144, 2064), (4000, 80, 656)]
 
 
