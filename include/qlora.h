@@ -328,9 +328,12 @@ QLORA_API qlora_status fp8_quantize(const qlora_bf16* w, int64_t n_out, int64_t 
  *   fp8_matmul:    Y  = x W^T  from x  [M, k_in]  -> Y  [M, n_out]
  *   fp8_matmul_t:  dX = dY W   from dY [M, n_out] -> dX [M, k_in]
  * with the values the codes and scales stand for, any finite fp32 scales (not
- * only the quantisers' powers of two), fp32 sums and one rounding to bf16.  A NaN
- * or infinite value in a row of x makes that row of the output NaN or infinite
- * and touches no other row.  k_in % 16 == 0, n_out % 16 == 0. */
+ * only the quantisers' powers of two) whose products of a row's and a weight
+ * block's scale stay in binary32's normal range, fp32 sums and one rounding to
+ * bf16.  A NaN or infinite value in a row of x makes that row of the output NaN
+ * or infinite and touches no other row.  The workspace holds the status word and,
+ * where a long reduction is cut into parts, their fp32 sums.  Results are bitwise
+ * reproducible for given sizes on a given GPU.  k_in % 16 == 0, n_out % 16 == 0. */
 QLORA_API size_t fp8_matmul_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out);
 QLORA_API qlora_status fp8_matmul(const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* Y,
                                   void* workspace, size_t workspace_bytes, qlora_stream_t stream);
@@ -359,14 +362,15 @@ QLORA_API qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const ql
  *   H = bf16(X + R),  rstd = 1 / sqrt(mean_j H_j^2 + eps),  Y = H * rstd * g,
  *   Y8 = fp8_quantize_rows(Y),  g = w or 1 + w as qlora_rmsnorm_fwd.
  * R and H may both be NULL (H is then X itself); one of Y and Y8 may be NULL.
- * H may be X or R (in place).  The sum of squares is held in binary64. d % 8 == 0. */
+ * H may be X or R (in place); otherwise no output overlaps an input.  The sum of
+ * squares is held in binary64.  d % 8 == 0. */
 QLORA_API qlora_status qlora_add_rmsnorm_fwd(const qlora_bf16* X, const qlora_bf16* R, const qlora_bf16* w, int64_t M,
                                              int64_t d, float eps, int32_t plus_one, qlora_bf16* H, qlora_bf16* Y,
                                              const qlora_fp8_rows* Y8, float* rstd, qlora_stream_t stream);
 /* Its backward with the norm weight frozen:
  *   dX = dH + rstd * (g * dY - n * mean_j(n_j g_j dY_j)),  n = H * rstd,
  * the gradient of X and of R alike.  dH [M, d] is the gradient that reaches H
- * past the norm (NULL: none).  dX may be dY or dH (in place). */
+ * past the norm (NULL: none).  dX may be dY or dH (in place), not H. */
 QLORA_API qlora_status qlora_add_rmsnorm_bwd(const qlora_bf16* H, const qlora_bf16* w, const float* rstd,
                                              const qlora_bf16* dY, const qlora_bf16* dH, int64_t M, int64_t d,
                                              int32_t plus_one, qlora_bf16* dX, qlora_stream_t stream);

@@ -261,6 +261,7 @@ def _check(fn, status):
 # is a good part of a small operator's: 28 -> 12 us for a norm of one token with four outputs)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
 def _stream():
@@ -414,7 +415,7 @@ class Workspace:
                 self.kept.append(self.buf)
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
             self.captured = False
-        if not self.captured and torch.cuda.is_current_stream_capturing():
+        if not self.captured and _capturing():
             self.captured = True
         return self.buf
 
@@ -775,7 +776,7 @@ def _fp8_matmul(fn, x, w, ws, out, transposed):
     M = x.codes.shape[0]
     cx = x.c("x", (M, red))
     if out is None:
-        out = torch.empty(M, cols, dtype=torch.bfloat16, device=x.codes.device)
+        out = x.codes.new_empty((M, cols), dtype=torch.bfloat16)
     else:
         _t(out, "out", (M, cols))
     _call_ws(fn, ws, lambda: fp8_matmul_workspace_bytes(M, k_in, n_out),
