@@ -138,16 +138,23 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPas
     const uint32_t ts = sb + b * stage_bytes, vs = ts + FW_T_BYTES;
 
     if constexpr (MODE != PASS_DA) {
-      // 8-bit rows (unless the caller has them): half a warp per row of the block
-      const int h = lane >> 4, c = (lane & 15) * 8, col = kb * 128 + c;
-      for (int i = warp * 2; a.codes && i < mt * 16; i += 16) {
-        const int m = i + h;
-        float f[8], s, inv;
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + b * stage_bytes + (m * FW_TP + c) * 2), f);
-        fp8_scale(half_warp_max(absmax8(f)), s, inv);
-        if (m < M) {
-          if (col < a.C) *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m0 + m) * a.C + col) = e4m3x8(f, inv);
-          if (c == 0) a.tscale[static_cast<size_t>(kb) * a.M + m0 + m] = s;
+      // 8-bit rows (unless the caller has them): half a warp per row of the block, four rows in flight
+      if (a.codes) {
+        const int h = lane >> 4, c = (lane & 15) * 8, col = kb * 128 + c;
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // rows past the staged ones hold stale bytes that nothing below uses
+          u[i] = *reinterpret_cast<const uint4*>(sm + b * stage_bytes + ((i * 16 + warp * 2 + h) * FW_TP + c) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = i * 16 + warp * 2 + h;
+          float f[8], s, inv;
+          unpack_bf16x8(u[i], f);
+          fp8_scale(half_warp_max(absmax8(f)), s, inv);
+          if (m < M) {
+            if (col < a.C) *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m0 + m) * a.C + col) = e4m3x8(f, inv);
+            if (c == 0) a.tscale[static_cast<size_t>(kb) * a.M + m0 + m] = s;
+          }
         }
       }
       // T V

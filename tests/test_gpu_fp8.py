@@ -178,11 +178,25 @@ LIN_SHAPES = [(1, 64, 16, 16, 1.0), (1, 1024, 528, 64, 0.25), (64, 4096, 1024, 6
               (20, 512, 400, 32, 0.5), (33, 1680, 144, 16, 1.0), (90, 144, 1680, 64, 0.25), (2050, 1296, 1296, 32, 0.5),
               # the few-row passes' ends: 64 and 65 rows, one block of columns and more than a cluster's, each rank
               (64, 272, 144, 32, 1.7), (65, 272, 144, 16, 0.5), (16, 4112, 2064, 64, 0.25), (48, 144, 6160, 16, 1.0),
-              (17, 128, 2064, 32, 1.0), (2, 16, 16, 64, 3.0)]
+              (17, 128, 2064, 32, 1.0), (2, 16, 16, 64, 3.0),
+              # the forward's one-launch pass and the general one, around their border
+              (256, 400, 144, 32, 0.5), (250, 2064, 144, 64, 1.0), (258, 400, 144, 64, 0.5)]
+
+
+@pytest.mark.parametrize("cap", [2, 10])
+@pytest.mark.parametrize("M,K,N,r,s", [(700, 640, 1296, 32, 0.5), (130, 1680, 1680, 16, 1.0), (2100, 1200, 1296, 64, 2.0)])
+def test_linear8_few_ctas(M, K, N, r, s, cap):
+    """The LoRA block between other tiles' blocks: every CTA pair walks many tiles or parts."""
+    ops.qlora_test_set_grid_cap(cap)
+    _check_linear8(M, K, N, r, s)
 
 
 @pytest.mark.parametrize("M,K,N,r,s", LIN_SHAPES)
 def test_linear8(M, K, N, r, s):
+    _check_linear8(M, K, N, r, s)
+
+
+def _check_linear8(M, K, N, r, s):
     X, dY, W, A, B = _linear(M, K, N, r, s, M + N)
     ws = ops.Workspace()
     w = ops.fp8_quantize(W.cuda())
