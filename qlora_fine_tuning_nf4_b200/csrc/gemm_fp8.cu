@@ -36,7 +36,8 @@
 //  * 160 columns with three accumulators, or two accumulators of 192: fewer
 //    stalls between accumulators, but 15-30% more bytes from L2 per product:
 //    0.38 ms;
-//  * sixteen accumulating warps, or packed pairs of fma: no gain.
+//  * sixteen accumulating warps: slower, 0.31 -> 0.33-0.345 ms; packed pairs of
+//    fma: no gain.
 #include "kernels.cuh"
 #include "ptx.cuh"
 

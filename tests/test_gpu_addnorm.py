@@ -113,7 +113,7 @@ def test_backward_by_differences():
 
 
 def test_special_values():
-    """An infinite or NaN element spoils its own row only; zero rows with eps = 0 give NaN as 0 * inf does."""
+    """An infinite or NaN element spoils its own row only; a row of zeros stays zeros."""
     X, R, w, _, _ = _inputs(6, 520, False, 2)
     X[1, 3], X[2, 500], X[4] = float("inf"), float("nan"), 0.0
     R[4] = 0.0
@@ -129,6 +129,36 @@ def test_special_values():
     back, ref = Y8.codes.double().cpu().numpy(), fp8.e4m3_values()[codes]
     assert np.array_equal(back, ref, equal_nan=True)
     assert np.array_equal(gpu_f64(Y8.scale), scale)
+
+
+@pytest.mark.parametrize("d", [40, 1208, 4096, 16392])
+def test_rstd_is_the_correctly_rounded_value(d):
+    """The sum of squares in binary64 and eps as the binary32 number that the call takes: rstd is the nearest binary32
+    number.  In any order, a sum of d exact positive squares is off by d 2^-53 relative at most, the mean, eps, root
+    and division by 2^-53 each; both sides carry that, so rows nearer than 2 (d + 4) 2^-53 to a border are left out."""
+    M = 4096
+    X, R, w, _, _ = (t.cuda() for t in _inputs(M, d, False, d))
+    H, _, rstd, _ = ops.qlora_add_rmsnorm_fwd(X, R, w, 1e-5)
+    ref = 1.0 / torch.sqrt(H.double().square().mean(1) + float(np.float32(1e-5)))
+    m = 2 * (d + 4) * 2.0 ** -53
+    lo, hi = (ref * (1 - m)).float(), (ref * (1 + m)).float()
+    assert torch.all((rstd == lo) | (rstd == hi))
+    # 4096 rows, each within m of a border with probability 2 m / 2^-24 at most: 0.5 rows expected at the widest d, and
+    # more than 8 with a probability below 1e-8
+    assert int((lo != hi).sum()) <= 8
+
+
+def test_zero_row_without_eps():
+    """eps = 0 is allowed: a row of zeros has rstd = 1 / 0 = inf and Y = 0 * inf = NaN; other rows are untouched by it."""
+    X, _, w, _, _ = _inputs(3, 264, False, 8)
+    X[1] = 0.0
+    H, Y, rstd, Y8 = ops.qlora_add_rmsnorm_fwd(X.cuda(), None, w.cuda(), 0.0, quantize=True)
+    assert torch.isinf(rstd[1]) and torch.isnan(Y[1]).all() and torch.isnan(Y8.codes[1].float()).all()
+    for m in (0, 2):
+        s = slice(m, m + 1)
+        _check_fwd(X[s], None, w, 0.0, False, H[s].contiguous(), Y[s], rstd[s], None)
+        codes, _ = fp8.quantize_rows(gpu_f64(Y[s]))
+        assert np.array_equal(Y8.codes[s].view(torch.uint8).cpu().numpy(), codes)
 
 
 def test_many_rows_same_as_one_by_one():
