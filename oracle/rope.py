@@ -1,7 +1,7 @@
 """Rotary positions in fp64 numpy (oracle; test infrastructure only).
 
 Pair i of a head turns by position * freq[i] radians; the pairs are (2i, 2i + 1) (interleaved) or (i, i + rot / 2).
-The survey's pages name the operator and its derivative, the transposed rotation."""
+The derivative is the transposed rotation."""
 
 import numpy as np
 
