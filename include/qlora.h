@@ -345,7 +345,9 @@ QLORA_API qlora_status fp8_matmul_t(const qlora_fp8_rows* dY, const qlora_fp8* w
  *   XA = X A                                  -> XA_saved [M, r]
  *   Y  = q(X) W^T + s XA B                    -> Y [M, n_out]
  *   dX = q(dY) W + s (dY B^T) A^T,  dA = s X^T (dY B^T),  dB = s XA^T dY
- * q(.) is fp8_quantize_rows; the adapter's terms read the bf16 X and dY.  X8 is
+ * q(.) is fp8_quantize_rows; the adapter's terms read the bf16 X and dY.  The fp32
+ * sums s X A and s dY B^T enter Y, dX and dA with 16 bits; dB is that of XA_saved
+ * as it is given, the bf16 rounding of X A.  X8 is
  * X already quantised (qlora_add_rmsnorm_fwd writes it), or NULL: the call then
  * quantises X in its workspace.  k_in % 16 == 0, n_out % 16 == 0, r = 16, 32 or
  * 64. */

@@ -400,10 +400,11 @@ qlora_status pass_rowproj_bt(const bf16* T, int64_t M, int64_t N, const bf16* B,
 // Supported factor-tile widths of the colproj kernel: R rounded up to 16, 32, 64 or 128.
 int colproj_width(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
 
-// Q = T^T U (U [M, R] with row stride ldu, R <= 128) -> outs
+// Q = T^T U (U [M, R] with row stride ldu, R <= 128) -> outs; `fold`: U = [U0 | U1], R a tile width, and
+// Q = T^T (U0 + U1)
 qlora_status pass_colproj(const bf16* T, int64_t M, int64_t ncols, const bf16* U, int R, float* part,
                           ReduceOuts outs, int* status, cudaStream_t st, int64_t ldt = 0, int64_t ldu = 0,
-                          ReduceBatch* batch = nullptr) {
+                          ReduceBatch* batch = nullptr, bool fold = false) {
   CUtensorMap mt, mu;
   if (!map_bf16(&mt, T, ncols, M, ldt ? ldt : ncols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) return QLORA_ERR_CUDA;
   if (!map_factor(&mu, U, M, R, ldu ? ldu : R, colproj_width(R))) return QLORA_ERR_CUDA;
@@ -413,6 +414,7 @@ qlora_status pass_colproj(const bf16* T, int64_t M, int64_t ncols, const bf16* U
   const int64_t nch = cdiv(ncols, 64);
   ReduceJob j = reduce_job(part, cdiv(nch, cc), cc * 64, ncols, R, planned_slot_cap(p.slot_cap), 0, p.sp, outs);
   j.status = status;
+  j.fold = fold ? 1 : 0;
   {
     KScope k(K_COLPROJ, st);
     const qlora_status s = cuda_status(launch_colproj(R, cc, mt, mu, j, (int)cdiv(M, 64), (int)nch, status, st));
@@ -454,11 +456,11 @@ qlora_status pass_dypass(const bf16* T, int64_t M, int64_t N, const bf16* U, con
 
 // One reduction output: columns [col0, col0 + width) of the partials, scaled, bf16
 // into p (row stride ld, or transposed).
-ReduceOut rout(bf16* p, int col0, int width, int ld, int transpose, float scale) {
-  return {p, col0, width, ld, transpose, scale};
+// `rest`: not the rounded value but what the rounding leaves.
+ReduceOut rout(bf16* p, int col0, int width, int ld, int transpose, float scale, int rest = 0) {
+  return {p, col0, width, ld, transpose, scale, rest};
 }
-ReduceOuts routs(ReduceOut a, ReduceOut b = {nullptr, 0, 0, 0, 0, 0.f}, ReduceOut c = {nullptr, 0, 0, 0, 0, 0.f},
-                 ReduceOut d = {nullptr, 0, 0, 0, 0, 0.f}) {
+ReduceOuts routs(ReduceOut a, ReduceOut b = {}, ReduceOut c = {}, ReduceOut d = {}) {
   ReduceOuts o;
   o.o[0] = a;
   o.o[1] = b;
@@ -1483,8 +1485,8 @@ size_t fp8_part_bytes(int64_t M, int64_t red, int64_t out) {
   const Fp8Plan p = plan_fp8(M, red, out);
   return !p.few && p.splits > 1 ? static_cast<size_t>(p.splits) * cdiv(M, 256) * 256 * out * 4 : 0;
 }
-// D = x W^T (bwd = false) or x W, plus L Rt with the LoRA operands L [M, r] and B [r, n_out] or
-// A [k_in, r] (r = 0: none).  `part` has room for fp8_part_bytes.
+// D = x W^T (bwd = false) or x W, plus (L0 + L1) Rt with the LoRA operands L = [L0 | L1] [M, 2 r] and
+// B [r, n_out] or A [k_in, r] (r = 0: none).  `part` has room for fp8_part_bytes.
 qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const qlora_fp8& w, int64_t M, bf16* D,
                       const bf16* L, const bf16* Rf, int r, float* part, int* status, cudaStream_t st) {
   const int64_t K = w.k_in, N = w.n_out;
@@ -1500,7 +1502,7 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
     const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
     if (!make_map(&m.w, u8, 1, w.codes, K, N, K, 128, 128, swz) || !make_map(&m.x, u8, 1, codes, red, M, red, 128, nt, swz))
       return QLORA_ERR_CUDA;
-    if (r > 0 && (!map_bf16(&m.l, L, r, M, r, 64, nt, swz) ||
+    if (r > 0 && (!map_bf16(&m.l, L, 2 * r, M, 2 * r, 64, nt, swz) ||
                   !(bwd ? map_bf16(&m.r, Rf, r, K, r, 64, 128, swz) : map_bf16(&m.r, Rf, N, r, N, 64, 64, swz))))
       return QLORA_ERR_CUDA;
     KScope k(bwd ? K_GEMM8_BWD : K_GEMM8_FWD, st);
@@ -1519,7 +1521,7 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
   if (plan.splits > 1 && !make_map(&maps.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, out, prows * plan.splits, out,
                                    32, 16, CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
-  if (r > 0 && (!map_bf16(&maps.la, L, r, M, r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (r > 0 && (!map_bf16(&maps.la, L, 2 * r, M, 2 * r, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
                 !(bwd ? map_bf16(&maps.lb, Rf, r, K, r, 64, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B)
                       : map_bf16(&maps.lb, Rf, N, r, N, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))))
     return QLORA_ERR_CUDA;
@@ -1581,7 +1583,10 @@ namespace {
 // it saves two launches (128 rows, rank 64: 21.6 vs 23.7 us; 2048 rows, whose passes are bound by
 // bandwidth, 67.6 vs 49.3 us).
 constexpr int64_t kOnePassRows = 64, kFwdPassRows = 256;
-// Workspace of an e4m3 projection: [status word | 256 B][M x r vector][row codes][row scales][partials].
+// Workspace of an e4m3 projection: [status word | 256 B][M x 2r: the pair of s XA or s G][row codes][row
+// scales][partials].  The pair (the bf16 rounding of an fp32 sum, and what it leaves) carries the sum to 2^-16
+// of it into Y, dX and dA: one rounding alone gave dA sqrt(2) of the error that its own rounding has.  It costs
+// one more block per product and twice the columns of the dA pass.
 // At ranks 32 and 64 the backward reduces its dB and dA passes in one launch at the end, so their
 // partials stay apart from those of the passes between: [dB][dA][the rest].
 struct Linear8Ws {
@@ -1591,14 +1596,14 @@ Linear8Ws linear8_ws(int64_t M, int64_t K, int64_t N, int r) {
   Linear8Ws w;
   const int64_t wide = std::max(K, N);
   w.vec = 256;
-  w.codes = w.vec + align256(static_cast<size_t>(M) * r * 2);
+  w.codes = w.vec + align256(static_cast<size_t>(M) * 2 * r * 2);
   w.scale = w.codes + align256(static_cast<size_t>(M) * wide);
   w.db = w.scale + align256(static_cast<size_t>(M) * cdiv(wide, 128) * 4);
   w.da = w.db + (r == 16 ? 0 : align256(colproj_part_bytes(M, N, r)));
-  w.part = w.da + (r == 16 ? 0 : align256(colproj_part_bytes(M, K, r)));
+  w.part = w.da + (r == 16 ? 0 : align256(colproj_part_bytes(M, K, 2 * r)));
   size_t part = rowproj_part_bytes(M, K, r);
   part = std::max(part, dypass_part_bytes(M, N, r));
-  part = std::max(part, colproj_part_bytes(M, K, r));
+  part = std::max(part, colproj_part_bytes(M, K, 2 * r));
   part = std::max(part, std::max(fp8_part_bytes(M, K, N), fp8_part_bytes(M, N, K)));
   w.total = w.part + align256(part);
   return w;
@@ -1656,12 +1661,12 @@ qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* 
   if (!X8 && (s = fp8_quantize_rows(X, M, K, reinterpret_cast<uint8_t*>(w + l.codes),
                                     reinterpret_cast<float*>(w + l.scale), stream)) != QLORA_OK)
     return s;
-  bf16* xa = reinterpret_cast<bf16*>(XA_saved);
-  const bool scaled = lin->scale != 1.0f;
-  bf16* XAs = scaled ? reinterpret_cast<bf16*>(w + l.vec) : xa;
+  bf16* XAs = reinterpret_cast<bf16*>(w + l.vec);
   s = pass_rowproj(reinterpret_cast<const bf16*>(X), M, K, reinterpret_cast<const bf16*>(lin->A), nullptr, r,
                    reinterpret_cast<float*>(w + l.part),
-                   routs(rout(xa, 0, r, r, 0, 1.f), rout(scaled ? XAs : nullptr, 0, r, r, 0, lin->scale)), status, st);
+                   routs(rout(reinterpret_cast<bf16*>(XA_saved), 0, r, r, 0, 1.f),
+                         rout(XAs, 0, r, 2 * r, 0, lin->scale), rout(XAs + r, 0, r, 2 * r, 0, lin->scale, 1)),
+                   status, st);
   if (s != QLORA_OK) return s;
   return gemm_fp8(false, codes, scale, lin->w, M, reinterpret_cast<bf16*>(Y), XAs,
                   reinterpret_cast<const bf16*>(lin->B), r, reinterpret_cast<float*>(w + l.part), status, st);
@@ -1711,7 +1716,7 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
     return cuda_status(launch_pass_da(x, (int)M, (int)K, sG, r, reinterpret_cast<bf16*>(dA), num_sms(), st));
   }
   if ((s = fp8_quantize_rows(dY, M, N, codes, scale, stream)) != QLORA_OK) return s;
-  const ReduceOuts gouts = routs(rout(sG, 0, r, r, 0, sc));
+  const ReduceOuts gouts = routs(rout(sG, 0, r, 2 * r, 0, sc), rout(sG + r, 0, r, 2 * r, 0, sc, 1));
   const ReduceOuts bouts = routs(rout(reinterpret_cast<bf16*>(dB), 0, r, (int)N, 1, sc));
   const ReduceOuts aouts = routs(rout(reinterpret_cast<bf16*>(dA), 0, r, r, 0, 1.f));
   // G = dY B^T (stored scaled), dB = s (X A)^T dY, from the unquantised dY
@@ -1727,8 +1732,8 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
   s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG, reinterpret_cast<const bf16*>(lin->A),
                r, part, status, st);
   if (s != QLORA_OK) return s;
-  if (r == 16) return pass_colproj(x, M, K, sG, r, part, aouts, status, st);
-  s = pass_colproj(x, M, K, sG, r, reinterpret_cast<float*>(w + l.da), aouts, status, st, 0, 0, &rb);
+  if (r == 16) return pass_colproj(x, M, K, sG, 2 * r, part, aouts, status, st, 0, 0, nullptr, true);
+  s = pass_colproj(x, M, K, sG, 2 * r, reinterpret_cast<float*>(w + l.da), aouts, status, st, 0, 0, &rb, true);
   return s != QLORA_OK ? s : flush_reduce(rb, st);
 }
 

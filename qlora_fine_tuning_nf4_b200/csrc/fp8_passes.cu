@@ -2,6 +2,8 @@
 //   forward   q(X), XA = X A                       (PASS_FWD, any M)
 //   backward  q(dY), G = dY B^T, dB = s XA^T dY    (PASS_DY, M <= 64)
 //             dA = X^T (s G)                       (PASS_DA, M <= 64)
+// s X A and s G leave as pairs of bf16 numbers (the rounded sum and what the rounding
+// leaves, 16 bits together) for the products that go on from them.
 // each in one launch that reads T once, for the row counts that launches bound: the
 // general path runs a quantiser, one or two passes with fp32 partials and a reduction
 // for each of them (64 rows, rank 64, 4096 -> 1024: 12 launches a step, 44 us; here 6,
@@ -24,13 +26,13 @@ constexpr int FW_T_BYTES = FW_ROWS * FW_TP * 2;
 constexpr int FW_STAGES = 4;
 enum PassMode : int { PASS_FWD = 0, PASS_DY = 1, PASS_DA = 2 };
 // Bytes of a stage (a block of T and of the factor: [128][r + 8] forward, [r][128 + 8] backward), of U
-// [64][r + 8], and of the low-rank sums [64][r + 8] of the four reduction shares, which take the
-// stages' place once these are done with.
+// ([64][r + 8], the pair [64][2 r + 8] for dA), and of the low-rank sums [64][r + 8] of the four reduction
+// shares, which take the stages' place once these are done with.
 __host__ __device__ constexpr int fw_stage_bytes(int mode, int r) {
   return FW_T_BYTES + (mode == PASS_FWD ? 128 * (r + 8) * 2 : (mode == PASS_DA ? 0 : r * FW_TP * 2));
 }
 __host__ __device__ constexpr int fw_u_bytes(int mode, int r) {
-  return mode == PASS_FWD ? 0 : FW_ROWS * (r + 8) * 2;
+  return mode == PASS_FWD ? 0 : FW_ROWS * ((mode == PASS_DA ? 2 * r : r) + 8) * 2;
 }
 __host__ __device__ constexpr int fw_smem(int mode, int r) {
   return FW_STAGES * fw_stage_bytes(mode, r) + fw_u_bytes(mode, r);
@@ -45,8 +47,8 @@ struct RankPass {
   uint8_t* codes;    // q(T): [M, C]; null: not wanted
   float* tscale;     // [ceil(C / 128), M]
   const bf16* V;     // low-rank factor: A [C, r] (forward) or B [r, C] (backward)
-  bf16 *low, *lows;  // T V and scale * T V as [M, r]; either may be null
-  const bf16* U;     // [M, r]: XA or s G
+  bf16 *low, *lows;  // T V [M, r] and scale * T V [M, 2 r] (the pair); either may be null
+  const bf16* U;     // [M, r]: XA, or [M, 2 r]: the pair of s G
   bf16* outer;       // dB [r, C] (scaled) or dA [C, r]
   float scale;
   int cluster;       // CTAs per 64 rows
@@ -107,10 +109,11 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPas
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
   const uint32_t us = sb + FW_STAGES * stage_bytes;
+  const int ur = MODE == PASS_DA ? 2 * r : r, ulc = MODE == PASS_DA ? lc + 1 : lc;  // U's columns
   if constexpr (MODE != PASS_FWD) {
-    for (int i = tid; i < (mt * 16) << lc; i += FW_THREADS) {
-      const int m = i >> lc, c = (i - (m << lc)) * 8;
-      cp_async16(us + (m * (r + 8) + c) * 2, a.U + (m < M ? static_cast<size_t>(m) * r + c : 0), m < M);
+    for (int i = tid; i < (mt * 16) << ulc; i += FW_THREADS) {
+      const int m = i >> ulc, c = (i - (m << ulc)) * 8;
+      cp_async16(us + (m * (ur + 8) + c) * 2, a.U + (m < M ? static_cast<size_t>(m) * ur + c : 0), m < M);
     }
   }
   for (int s = 0; s < FW_STAGES - 1; ++s) {  // a group per stage, empty past the last block
@@ -242,10 +245,13 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPas
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           if (j * 8 >= r) break;
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4_t(us + ((t * 16 + (mi & 1) * 8 + mr) * (r + 8) + j * 8 + (mi >> 1) * 8) * 2, b0, b1, b2, b3);
-          mma_bf16_16816(o[j], a0, a1, a2, a3, b0, b1);
-          mma_bf16_16816(o[j + 1], a0, a1, a2, a3, b2, b3);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // the pair's halves
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(us + ((t * 16 + (mi & 1) * 8 + mr) * (ur + 8) + h * r + j * 8 + (mi >> 1) * 8) * 2, b0, b1, b2, b3);
+            mma_bf16_16816(o[j], a0, a1, a2, a3, b0, b1);
+            mma_bf16_16816(o[j + 1], a0, a1, a2, a3, b2, b3);
+          }
         }
       }
 #pragma unroll
@@ -308,12 +314,16 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPas
 #pragma unroll
         for (int i = 0; i < 8; ++i) v.x += x[i].x, v.y += x[i].y, v.z += x[i].z, v.w += x[i].w;
       }
-      const size_t o = static_cast<size_t>(m0 + m) * r + c;
       if (a.low)
-        *reinterpret_cast<uint2*>(a.low + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      if (a.lows)
-        *reinterpret_cast<uint2*>(a.lows + o) =
-            make_uint2(pack_bf16x2(v.x * a.scale, v.y * a.scale), pack_bf16x2(v.z * a.scale, v.w * a.scale));
+        *reinterpret_cast<uint2*>(a.low + static_cast<size_t>(m0 + m) * r + c) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (a.lows) {
+        bf16* o = a.lows + static_cast<size_t>(m0 + m) * 2 * r + c;
+        v.x *= a.scale, v.y *= a.scale, v.z *= a.scale, v.w *= a.scale;
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        *reinterpret_cast<uint2*>(o + r) = make_uint2(pack_bf16x2(bf16_rest(v.x), bf16_rest(v.y)),
+                                                      pack_bf16x2(bf16_rest(v.z), bf16_rest(v.w)));
+      }
     }
     cluster_sync();  // no CTA leaves while another still reads its sums
   }
@@ -363,18 +373,18 @@ static cudaError_t launch_pass(RankPass a, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// q(X) and XA (low), s XA (lows)
+// q(X) and XA (low), the pair of s XA (lows)
 cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
                             bf16* low, bf16* lows, int sms, cudaStream_t st) {
   return launch_pass<PASS_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale, 1}, sms, st);
 }
-// q(dY), s G (lows) and dB = s XA^T dY, M <= 64
+// q(dY), the pair of s G (lows) and dB = s XA^T dY, M <= 64
 cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
                            bf16* lows, const bf16* XA, bf16* dB, int sms, cudaStream_t st) {
   if (M > FW_ROWS) return cudaErrorInvalidValue;
   return launch_pass<PASS_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale, 1}, sms, st);
 }
-// dA = X^T (s G), M <= 64
+// dA = X^T (s G) from the pair of s G, M <= 64
 cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st) {
   if (M > FW_ROWS) return cudaErrorInvalidValue;
   return launch_pass<PASS_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f, 1}, sms, st);

@@ -18,8 +18,10 @@
 //   warps 4-11   accumulate: TMEM -> scale -> registers; at the tile's end
 //                registers -> bf16 -> shared memory -> TMA store
 // Two TMEM accumulators of 256 columns alternate per reduction block, so the MMA
-// of one block runs while the previous one is being added.  The LoRA term is one
-// more block: bf16 operands (kind::f16) and scale 1.
+// of one block runs while the previous one is being added.  The LoRA term is two
+// more blocks with bf16 operands (kind::f16) and scale 1: the fp32 sums s X A (or
+// s dY B^T) come as a pair of bf16 numbers, the rounded value and what the rounding
+// leaves, each times the same factor, so that they enter Y (or dX) with 16 bits.
 //
 // What bounds it.  Per block and SM the tensor core needs 512 cycles, 32 KB come
 // from L2 (64 bytes a cycle: 512 as well), and the accumulating warps 256 cycles
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(Gemm8Cfg<BN>::THREADS, 1)
   grid_dep_launch();
 
   // Tiles in groups of group_m row tiles, rows fastest inside a group (as the bf16 GEMM); a tile's
-  // parts side by side.  Blocks [k0, k1) of the reduction; the last part takes the LoRA block (nkb).
+  // parts side by side.  Blocks [k0, k1) of the reduction; the last part takes the LoRA blocks (nkb, nkb + 1).
   auto unit_coords = [&](int u, int& m0, int& n0, int& k0, int& k1) {
     const int t = u / args.splits, p = u - t * args.splits;
     const int gsz = args.group_m * n_tiles;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(Gemm8Cfg<BN>::THREADS, 1)
     n0 = (r / gm) * C::BNT;
     k0 = static_cast<int>(static_cast<int64_t>(args.nkb) * p / args.splits);
     k1 = static_cast<int>(static_cast<int64_t>(args.nkb) * (p + 1) / args.splits);
-    if (p == args.splits - 1 && args.lora_k16 > 0) ++k1;
+    if (p == args.splits - 1 && args.lora_k16 > 0) k1 += 2;
   };
 
   if (warp < C::EPI_WARP0) {
@@ -180,9 +182,9 @@ __global__ void __launch_bounds__(Gemm8Cfg<BN>::THREADS, 1)
               if (BWD) tma_load_2d_pair(b, &maps.b, bar, col, kb * C::BK);
               else tma_load_2d_pair(b, &maps.b, bar, kb * C::BK, col);
             } else {
-              // LoRA operands, 64 wide with zeros beyond the rank: A [BNC columns, r] K-major (dX), or
-              // B [r, BNC columns] MN-major in chunks of 64 columns (forward)
-              tma_load_2d_pair(a, &maps.la, bar, 0, m0);
+              // LoRA operands, 64 wide (the MMAs read the rank's): half kb - nkb of the pair, and A [BNC
+              // columns, r] K-major (dX) or B [r, BNC columns] MN-major in chunks of 64 columns (forward)
+              tma_load_2d_pair(a, &maps.la, bar, (kb - args.nkb) * args.lora_k16 * 16, m0);
               if (BWD) {
                 tma_load_2d_pair(b, &maps.lb, bar, 0, col);
               } else {

@@ -12,8 +12,8 @@
 //   warps 4-7    accumulate: TMEM -> scale -> registers
 // Eight accumulators of 16 to 64 columns hide the way from the MMA to the accumulating
 // warps and back.  The CTAs' sums meet through distributed shared memory, are added in
-// rank order and leave as bf16.  The LoRA term is one more block of the last CTA: bf16
-// operands (kind::f16) and scale 1.
+// rank order and leave as bf16.  The LoRA term is two more blocks of the last CTA, the
+// halves of the low-rank pair (gemm_fp8.cu): bf16 operands (kind::f16) and scale 1.
 //
 // With weights that come from HBM: one row, 4096 -> 14336 (59 MB, 9.1 us at the copy
 // rate) 12.9 us, 4096 -> 4096 (17 MB, 2.6 us) 6.5 us; 64 rows 16.2 and 8.5 us.  Warp-level
@@ -52,7 +52,7 @@ struct FewArgs {
   int sb_k, sb_n;
   int M, nkb, cols;   // rows, reduction blocks, output columns
   int cluster;        // CTAs that share a tile's reduction
-  int lora_k16;       // 16-wide reduction steps of the LoRA operands (rank / 16), 0 = no adapter
+  int lora_k16;       // 16-wide reduction steps of a LoRA block (rank / 16), 0 = no adapter
   bf16* out;          // [M, cols]
   int* status;
 };
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
   const int rank = static_cast<int>(blockIdx.x % a.cluster);
   const int n0 = static_cast<int>(blockIdx.x / a.cluster) * C::BM;
   const int own = (a.nkb - rank + a.cluster - 1) / a.cluster;  // blocks rank, rank + cluster, ...
-  const int mine = own + (a.lora_k16 > 0 && rank == a.cluster - 1 ? 1 : 0);
+  const int mine = own + (a.lora_k16 > 0 && rank == a.cluster - 1 ? 2 : 0);
 
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -128,15 +128,15 @@ __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
           else tma_load_2d(w, &maps.w, full_bar(s), kb * 128, n0);
           tma_load_2d(x, &maps.x, full_bar(s), kb * 128, 0);
         } else {
-          // LoRA operands, 64 wide with zeros beyond the rank: A [128 columns, r] K-major (dX), or
-          // B [r, 128 columns] MN-major in chunks of 64 columns (forward)
+          // LoRA operands, 64 wide (the MMAs read the rank's): A [128 columns, r] K-major (dX) or
+          // B [r, 128 columns] MN-major in chunks of 64 columns (forward), and half i - own of the pair
           if (BWD) {
             tma_load_2d(w, &maps.r, full_bar(s), 0, n0);
           } else {
             tma_load_2d(w, &maps.r, full_bar(s), n0, 0);
             tma_load_2d(w + 8192, &maps.r, full_bar(s), n0 + 64, 0);
           }
-          tma_load_2d(x, &maps.l, full_bar(s), 0, 0);
+          tma_load_2d(x, &maps.l, full_bar(s), (i - own) * a.lora_k16 * 16, 0);
         }
       }
       __syncwarp();
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
 #pragma unroll
       for (int g = 0; g < C::G; ++g) {
         const int kb = rank + (i0 + g) * a.cluster;
-        const float lora = i0 + g == own ? 1.f : 0.f;
+        const float lora = i0 + g >= own ? 1.f : 0.f;
         const float w = kb < a.nkb ? __ldg(sb + static_cast<size_t>(kb) * a.sb_k) : 0.f;
 #pragma unroll
         for (int h = 0; h < NT / 32 + (NT < 32); ++h) {

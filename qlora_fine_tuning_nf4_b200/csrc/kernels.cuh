@@ -72,7 +72,7 @@ struct GemmArgs {
 struct Gemm8Maps {
   CUtensorMap a;    // A operand: e4m3 [M, reduction], box {128, 128}, 128B swizzle
   CUtensorMap b;    // weight: e4m3 [n_out, k_in], box {128, bn / 2}, 128B swizzle (forward), or {bn / 2, 128} (dX)
-  CUtensorMap la;   // LoRA left operand s*XA or s*G: bf16 [M, r], box {64, 128}
+  CUtensorMap la;   // LoRA left operand s*XA or s*G: bf16 [M, 2 r] (rounded | what that leaves), box {64, 128}
   CUtensorMap lb;   // LoRA right operand: B [r, N] (forward), box {64, 64}, or A [N, r] (dX), box {64, bn / 2}
   CUtensorMap out;  // output: bf16 [M, N], box {32, 32}, 64B swizzle
   CUtensorMap part; // splits > 1: fp32 [splits * prows, N], box {32, 16}, 128B swizzle
@@ -80,7 +80,7 @@ struct Gemm8Maps {
 struct Gemm8Args {
   int M, N;             // output rows and columns
   int nkb;              // 128-wide reduction blocks
-  int lora_k16;         // 16-wide reduction steps of the LoRA operand (rank / 16), 0 = no adapter
+  int lora_k16;         // 16-wide reduction steps of each LoRA block (rank / 16), 0 = no adapter
   const float* sa;      // [nkb, M]
   const float* sb;      // block scales of the weight
   int sb_k, sb_n;       // their strides per reduction block and per 128 output columns
@@ -95,7 +95,7 @@ struct Gemm8Args {
 struct FewMaps {
   CUtensorMap w;  // weight: e4m3 [n_out, k_in], box {128, 128}, 128B swizzle (all four)
   CUtensorMap x;  // rows: e4m3 [M, reduction], box {128, NT}
-  CUtensorMap l;  // LoRA left operand: bf16 [M, r], box {64, NT}
+  CUtensorMap l;  // LoRA left operand: bf16 [M, 2 r] (rounded | what that leaves), box {64, NT}
   CUtensorMap r;  // LoRA right operand: B [r, n_out], box {64, 64} (forward), or A [k_in, r], box {64, 128} (dX)
 };
 
@@ -137,6 +137,7 @@ struct ReduceOut {
   int ld;         // row stride of the destination (elements)
   int transpose;  // 0: dst[row * ld + c], 1: dst[c * ld + row]
   float scale;
+  int rest;       // 1: what the rounding of the value to bf16 leaves (0 where that is not finite)
 };
 struct ReduceOuts {
   ReduceOut o[4];
@@ -145,10 +146,11 @@ struct ReduceOuts {
 // Partials of one output of a skinny pass: part[g][slot][row in group][R] for
 // `groups` groups of `grows` rows (the last may extend past `rows`), slot_cap
 // slots per group; group g has `nslots` slots if nslots > 0, else
-// sk_slots(sp, g).  The reduction adds them in slot order and stores `outs`.
+// sk_slots(sp, g).  The reduction adds them in slot order and stores `outs`; with
+// `fold`, columns c and c + R / 2 are two parts of one sum (outs then count R / 2).
 struct ReduceJob {
   float* part;
-  int groups, grows, rows, R, slot_cap, nslots;
+  int groups, grows, rows, R, slot_cap, nslots, fold;
   SkPart sp;
   ReduceOuts outs;
   int* status;  // device status word (the checked build's bounds checks report there)

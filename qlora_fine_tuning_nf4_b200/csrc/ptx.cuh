@@ -392,5 +392,11 @@ QL_DEV uint32_t pack_bf16x2(float lo, float hi) {
 }
 QL_DEV float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 QL_DEV float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// What rounding v to bf16 leaves: with it as a second bf16 number the pair holds v to 2^-16 of it.
+// 0 where the rounded value is infinite or NaN: the first number then says it all.
+QL_DEV float bf16_rest(float v) {
+  const float r = bf16_lo(pack_bf16x2(v, 0.f));
+  return fabsf(r) < __uint_as_float(0x7F800000u) ? v - r : 0.f;
+}
 
 }  // namespace ql

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(SK_THREADS) dypass_kernel(const __grid_constan
 // [start[k], start[k + 1]).
 struct ReduceJobs {
   ReduceJob j[kMaxReduceJobs];
-  int start[kMaxReduceJobs + 1];  // prefix sums of rows * R / 4 (float4 elements)
+  int start[kMaxReduceJobs + 1];  // prefix sums of rows * R / 4 (float4 elements; R / 8 where folded)
   int n;                          // jobs in use
 };
 __global__ void __launch_bounds__(256) reduce_kernel(const __grid_constant__ ReduceJobs js) {
@@ -433,25 +433,28 @@ __global__ void __launch_bounds__(256) reduce_kernel(const __grid_constant__ Red
   while (k + 1 < js.n && idx >= js.start[k + 1]) ++k;
   idx -= js.start[k];
   const ReduceJob& j = js.j[k];
-  const int row = (idx * 4) / j.R, c = (idx * 4) % j.R;
+  const int cols = j.fold ? j.R / 2 : j.R;
+  const int row = (idx * 4) / cols, c = (idx * 4) % cols;
   const int g = row / j.grows, r = row % j.grows;
   int ns = j.nslots > 0 ? j.nslots : sk_slots(j.sp, g);
   if (!dev_check(g < j.groups && ns <= j.slot_cap, j.status)) ns = g < j.groups ? j.slot_cap : 0;
   const size_t slot_stride = static_cast<size_t>(j.grows) * j.R;
   const float* p = j.part + static_cast<size_t>(g) * j.slot_cap * slot_stride + static_cast<size_t>(r) * j.R + c;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < ns; s += 16) {
-    float4 v[16];
+  for (int half = 0; half < (j.fold ? 2 : 1); ++half, p += cols) {
+    for (int s = 0; s < ns; s += 16) {
+      float4 v[16];
 #pragma unroll
-    for (int t = 0; t < 16; ++t)
-      if (s + t < ns) v[t] = __ldg(reinterpret_cast<const float4*>(p + (s + t) * slot_stride));
+      for (int t = 0; t < 16; ++t)
+        if (s + t < ns) v[t] = __ldg(reinterpret_cast<const float4*>(p + (s + t) * slot_stride));
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      if (s + t < ns) {
-        acc.x += v[t].x;
-        acc.y += v[t].y;
-        acc.z += v[t].z;
-        acc.w += v[t].w;
+      for (int t = 0; t < 16; ++t) {
+        if (s + t < ns) {
+          acc.x += v[t].x;
+          acc.y += v[t].y;
+          acc.z += v[t].z;
+          acc.w += v[t].w;
+        }
       }
     }
   }
@@ -460,8 +463,10 @@ __global__ void __launch_bounds__(256) reduce_kernel(const __grid_constant__ Red
     const ReduceOut& o = j.outs.o[q];
     if (o.ptr == nullptr || c < o.col0 || c >= o.col0 + o.width) continue;
     const int cc = c - o.col0;
-    const bf16 b0 = __float2bfloat16_rn(o.scale * acc.x), b1 = __float2bfloat16_rn(o.scale * acc.y);
-    const bf16 b2 = __float2bfloat16_rn(o.scale * acc.z), b3 = __float2bfloat16_rn(o.scale * acc.w);
+    float4 v = make_float4(o.scale * acc.x, o.scale * acc.y, o.scale * acc.z, o.scale * acc.w);
+    if (o.rest) v = make_float4(bf16_rest(v.x), bf16_rest(v.y), bf16_rest(v.z), bf16_rest(v.w));
+    const bf16 b0 = __float2bfloat16_rn(v.x), b1 = __float2bfloat16_rn(v.y);
+    const bf16 b2 = __float2bfloat16_rn(v.z), b3 = __float2bfloat16_rn(v.w);
     if (o.transpose) {
       bf16* d = o.ptr + static_cast<size_t>(cc) * o.ld + row;
       d[0] = b0;
@@ -568,7 +573,7 @@ cudaError_t launch_reduce(const ReduceJob* jobs, int n, cudaStream_t st) {
   for (int k = 0; k < n; ++k) {
     js.j[k] = jobs[k];
     js.start[k] = static_cast<int>(total);
-    total += static_cast<int64_t>(jobs[k].rows) * jobs[k].R / 4;
+    total += static_cast<int64_t>(jobs[k].rows) * jobs[k].R / (jobs[k].fold ? 8 : 4);
   }
   if (total >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   js.start[n] = static_cast<int>(total);
