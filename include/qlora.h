@@ -365,7 +365,8 @@ QLORA_API qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const ql
  *   Y8 = fp8_quantize_rows(Y),  g = w or 1 + w as qlora_rmsnorm_fwd.
  * R and H may both be NULL (H is then X itself); one of Y and Y8 may be NULL.
  * H may be X or R (in place); otherwise no output overlaps an input.  The sum of
- * squares is held in binary64.  d % 8 == 0. */
+ * squares is held in binary64, so any finite row with rstd in binary32's range is
+ * normed.  d % 8 == 0. */
 QLORA_API qlora_status qlora_add_rmsnorm_fwd(const qlora_bf16* X, const qlora_bf16* R, const qlora_bf16* w, int64_t M,
                                              int64_t d, float eps, int32_t plus_one, qlora_bf16* H, qlora_bf16* Y,
                                              const qlora_fp8_rows* Y8, float* rstd, qlora_stream_t stream);

@@ -8,7 +8,8 @@
 // HBM-bound row kernels.  T threads hold one row in registers (16-byte loads,
 // all in flight at once), so every tensor is read or written once; 16
 // neighbouring threads hold one block of 128 columns, whose largest magnitude is
-// a half-warp shuffle.  The sum of squares is held in binary64: rstd is then the
+// a half-warp shuffle.  Squares and their sum are in binary64: a finite row keeps its
+// norm whatever its size (binary32 squares end at 2^64 and 2^-75), and rstd is the
 // correctly rounded value in nearly every row whatever the order of the sum, so y
 // and the 8-bit codes next to a rounding border do not depend on T (49 million
 // rows of 8 to 1024 columns against torch's binary64 mean: no rstd differed).  eps
@@ -61,7 +62,10 @@ QL_DEV void add_squares(const uint4& v, double& ss) {
   float f[8];
   unpack_bf16x8(v, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss += static_cast<double>(f[i] * f[i]);  // 16 significant bits: exact in fp32
+  for (int i = 0; i < 8; ++i) {
+    const double x = f[i];
+    ss = fma(x, x, ss);
+  }
 }
 // h -> y for eight elements; returns y as bf16, and as floats for the 8-bit output.
 QL_DEV uint4 norm8(const uint4& h, float rstd, const float (&g)[8], float (&y)[8]) {
