@@ -202,15 +202,16 @@ struct AddNormBwd {
   bf16* dX;             // may be dY or dH
 };
 
-QL_DEV float dot_gdy(const uint4& h, const uint4& dy, const float (&g)[8], float acc) {
+// n = h * rstd comes first: it is of the order of 1 where h, rstd or rstd^2 may leave binary32
+QL_DEV float dot_ngdy(const uint4& h, const uint4& dy, const float (&g)[8], float rstd, float acc) {
   float f[8], e[8];
   unpack_bf16x8(h, f);
   unpack_bf16x8(dy, e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc = fmaf(f[i] * g[i], e[i], acc);
+  for (int i = 0; i < 8; ++i) acc = fmaf(f[i] * rstd, g[i] * e[i], acc);
   return acc;
 }
-// dh + rstd * (g dy - h * cm), cm = rstd^2 * mean(h g dy)
+// dh + rstd * (g dy - h * cm), cm = rstd * mean(n g dy)
 QL_DEV uint4 norm_bwd8(const uint4& h, const uint4& dy, const uint4& dh, const float (&g)[8], float rstd, float cm) {
   float f[8], e[8], o[8];
   unpack_bf16x8(h, f);
@@ -249,10 +250,10 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) add_rmsnorm_bwd_kernel(cons
     if (c >= a.d) break;
     float g[8];
     norm_gain8(a.w, c, a.plus_one, g);
-    acc = dot_gdy(h[i], dy[i], g, acc);
+    acc = dot_ngdy(h[i], dy[i], g, rstd, acc);
   }
   acc = row_sum<T>(acc, red);
-  const float cm = rstd * rstd * __fdiv_rn(acc, static_cast<float>(a.d));
+  const float cm = rstd * __fdiv_rn(acc, static_cast<float>(a.d));
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * T + t) * 8;
@@ -275,11 +276,11 @@ __global__ void __launch_bounds__(AN_WIDE) add_rmsnorm_bwd_wide_kernel(const Add
   for (int c = threadIdx.x * 8; c < a.d; c += AN_WIDE * 8) {
     float g[8];
     norm_gain8(a.w, c, a.plus_one, g);
-    acc = dot_gdy(*reinterpret_cast<const uint4*>(a.H + off + c), *reinterpret_cast<const uint4*>(a.dY + off + c), g,
-                  acc);
+    acc = dot_ngdy(*reinterpret_cast<const uint4*>(a.H + off + c), *reinterpret_cast<const uint4*>(a.dY + off + c), g,
+                   rstd, acc);
   }
   acc = row_sum<AN_WIDE>(acc, red);
-  const float cm = rstd * rstd * __fdiv_rn(acc, static_cast<float>(a.d));
+  const float cm = rstd * __fdiv_rn(acc, static_cast<float>(a.d));
 #pragma unroll 2
   for (int c = threadIdx.x * 8; c < a.d; c += AN_WIDE * 8) {
     float g[8];

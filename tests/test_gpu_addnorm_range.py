@@ -1,4 +1,4 @@
-"""qlora_add_rmsnorm_fwd on finite rows whose squares leave binary32: beyond 2^64 and below 2^-75.
+"""qlora_add_rmsnorm_fwd / _bwd on finite rows whose squares leave binary32: beyond 2^64 and below 2^-75.
 
 Bounds as in test_gpu_addnorm.py: the formula has no other rounding at these magnitudes, since rstd (1e-25 to 1e25
 here) is a normal binary32 number and so is every product that the formula names."""
@@ -41,3 +41,18 @@ def test_forward(d, size, eps):
     codes, scale = fp8.quantize_rows(gpu_f64(Y))
     assert np.array_equal(Y8.codes.view(torch.uint8).cpu().numpy(), codes)
     assert np.array_equal(gpu_f64(Y8.scale), scale)
+
+
+@pytest.mark.parametrize("size", [1e25, 3e19, 1e-20, 1e-25])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_backward(d, size):
+    H, _, w, dY = _rows(d, size, d + 1)
+    h, wf, dy = (t.double().numpy() for t in (H, w, dY))
+    _, r = oracle.rmsnorm_fwd(h, wf, 0.0)
+    rstd = torch.tensor(r, dtype=torch.float32, device="cuda")
+    dX = ops.qlora_add_rmsnorm_bwd(H.cuda(), w.cuda(), rstd, dY.cuda())
+    ref = oracle.rmsnorm_bwd(h, wf, 0.0, dy)
+    n = h * r[:, None]
+    c = np.mean(np.abs(n * wf * dy), axis=1, keepdims=True)
+    slack = r[:, None] * (8 * U32 * (np.abs(wf * dy) + np.abs(n) * c) + (d + 8) * U32 * np.abs(n) * c)
+    assert np.all(np.abs(gpu_f64(dX) - ref) <= U16 * np.abs(ref) + (1 + U16) * slack)
