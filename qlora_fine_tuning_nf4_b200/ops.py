@@ -397,26 +397,59 @@ def _dims(lin):
     return (lin.w.n_out, lin.w.k_in) if isinstance(lin, LoraLinear) else (lin.n_out, lin.k_in)
 
 
+_growth_streams = {}  # device index -> stream on which buffers are zeroed while the current stream is being captured
+
+
+def _zeroed_outside_capture(nbytes, device):
+    """Zeroed bytes while the current stream is being captured.  Made there they would belong to the graph: zeroed by
+    each of its replays (with the status word in them) and by nothing before the first one, in memory that other
+    graphs of the pool write to.  So they are made on a stream that is not captured, and zero on return.  A thread
+    that captures may allocate and wait meanwhile in the relaxed capture mode only (CUDA's documentation of
+    cuThreadExchangeStreamCaptureMode)."""
+    exchange = ctypes.CDLL("libcuda.so.1").cuThreadExchangeStreamCaptureMode
+    mode = ctypes.c_int(2)  # CU_STREAM_CAPTURE_MODE_RELAXED; the call leaves the mode that was set
+    if exchange(ctypes.byref(mode)) != 0:
+        raise RuntimeError("cuThreadExchangeStreamCaptureMode failed")
+    try:
+        dev = _current_device()
+        if dev not in _growth_streams:
+            _growth_streams[dev] = torch.cuda.Stream()
+        with torch.cuda.stream(_growth_streams[dev]):
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _growth_streams[dev].synchronize()
+    finally:
+        exchange(ctypes.byref(mode))
+    return buf
+
+
 class Workspace:
-    """Caller-owned device workspace (zeroed once; grows on demand).
+    """Caller-owned device workspace (zeroed once; grows on demand, also while its calls are being captured).
 
     One workspace serves calls whose GPU work does not overlap: calls on one stream, or graphs replayed one after
-    the other.  Streams that run at the same time need one each.  A buffer that calls were captured with stays
-    alive after the workspace has grown, since a graph's replay still uses it."""
+    the other, in any order.  Streams that run at the same time need one each.  It has to outlive the graphs that
+    were captured with it; a buffer that calls were captured with stays alive after the workspace has grown, since
+    a graph's replay still uses it."""
 
     def __init__(self, device="cuda"):
         self.device = device
-        self.buf = torch.zeros(256, dtype=torch.uint8, device=device)
         self.captured, self.kept = False, []
+        self._make(256)
+
+    def _make(self, nbytes):
+        self.apart = bool(_capturing())  # made on a stream of its own
+        self.buf = (_zeroed_outside_capture(nbytes, self.device) if self.apart
+                    else torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
 
     def get(self, nbytes):
         if self.buf.numel() < nbytes:
             if self.captured:
                 self.kept.append(self.buf)
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self._make(nbytes)
             self.captured = False
         if not self.captured and _capturing():
             self.captured = True
+        elif self.apart and not _capturing():
+            self.buf.record_stream(torch.cuda.current_stream())  # its memory is not reused before this call is done
         return self.buf
 
 
