@@ -442,9 +442,12 @@ class Workspace:
 
     def get(self, nbytes):
         if self.buf.numel() < nbytes:
-            if self.captured:
-                self.kept.append(self.buf)
+            old = self.buf
             self._make(nbytes)
+            if self.captured or self.apart:  # a graph's replays use it, or its error (if any) cannot be copied now
+                self.kept.append(old)
+            else:
+                self.buf[:4].copy_(old[:4])  # an error recorded so far
             self.captured = False
         if not self.captured and _capturing():
             self.captured = True
@@ -1084,7 +1087,10 @@ def qlora_test_set_grid_cap(max_ctas):
 
 
 def qlora_last_device_status(ws: Workspace):
-    return int(lib().qlora_last_device_status(_p(ws.buf), _stream()))
+    """The error that calls with this workspace have recorded since it was last asked for (0: none), a timeout before
+    any other; waits for the current stream."""
+    found = [int(lib().qlora_last_device_status(_p(b), _stream())) for b in (ws.buf, *ws.kept)]
+    return 6 if 6 in found else max(found)  # QLORA_ERR_TIMEOUT
 
 
 def qlora_status_string(status):
