@@ -441,6 +441,8 @@ class Workspace:
                     else torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
 
     def get(self, nbytes):
+        if self.buf.get_device() != _current_device():
+            raise ValueError(f"the workspace is on {self.buf.device}, not on the current device cuda:{_current_device()}")
         if self.buf.numel() < nbytes:
             old = self.buf
             self._make(nbytes)
