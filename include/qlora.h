@@ -27,7 +27,10 @@
  *    synchronising.  The library never allocates device memory: the caller
  *    passes a workspace of at least the size the matching *_workspace_bytes
  *    query returns; its first 256 bytes hold the device status word and must
- *    be zeroed by the caller once before first use.
+ *    be zeroed by the caller once before first use.  A query answers for the M
+ *    it is asked about.  A smaller M may need more (work on few rows is split,
+ *    and the parts' fp32 sums take room): with several row counts, ask for each
+ *    and take the largest.
  *  - Invalid arguments are rejected on the host before anything is enqueued
  *    (QLORA_ERR_INVALID_ARG, _UNSUPPORTED_SHAPE, _MISALIGNED,
  *    _WORKSPACE_TOO_SMALL).  A failed launch returns QLORA_ERR_CUDA.  Errors
@@ -332,7 +335,8 @@ QLORA_API qlora_status fp8_quantize(const qlora_bf16* w, int64_t n_out, int64_t 
  * block's scale stay in binary32's normal range, fp32 sums and one rounding to
  * bf16.  A NaN or infinite value in a row of x makes that row of the output NaN
  * or infinite and touches no other row.  The workspace holds the status word and,
- * where a long reduction is cut into parts, their fp32 sums.  Results are bitwise
+ * where a long reduction is cut into parts, their fp32 sums: 4096 -> 4096 takes
+ * 256 bytes at 8192 rows and 8 MiB more at 128.  Results are bitwise
  * reproducible for given sizes on a given GPU.  k_in % 16 == 0, n_out % 16 == 0. */
 QLORA_API size_t fp8_matmul_workspace_bytes(int64_t M, int64_t k_in, int64_t n_out);
 QLORA_API qlora_status fp8_matmul(const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* Y,

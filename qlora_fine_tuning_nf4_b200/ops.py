@@ -800,6 +800,7 @@ def _call_ws(fn, ws, need, args):
 
 
 def fp8_matmul_workspace_bytes(M, K, N):
+    """For M rows; fewer rows may need more (a split reduction's partial sums), so ask for every M that is used."""
     return int(lib().fp8_matmul_workspace_bytes(M, K, N))
 
 
@@ -851,6 +852,7 @@ class LoraLinear8:
 
 
 def qlora_linear8_workspace_bytes(M, K, N, r=16):
+    """For M rows; fewer rows may need more, so ask for every M that is used."""
     return int(lib().qlora_linear8_workspace_bytes(M, K, N, r))
 
 
