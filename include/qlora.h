@@ -389,7 +389,10 @@ QLORA_API qlora_status qlora_add_rmsnorm_bwd(const qlora_bf16* H, const qlora_bf
  * for the pairs i < rot / 2 of each head: (2i, 2i + 1) if interleaved, else
  * (i, i + rot / 2).  The elements from rot on are copied (left alone in place).
  * turns [rot / 2] holds each pair's frequency in turns per position as a 64-bit
- * fraction; the angle is exact to 2^-34 turns at position 2^31.  positions [M]
+ * fraction.  position * turns[i] is exact modulo 2^64; the rotation takes its 32
+ * upper bits as a binary32 number, within 2^-26 + 2^-32 turns of it at any
+ * position.  What turns[i] itself is off by counts position times: 2^-34 turns at
+ * position 2^31 where it is the nearest 64-bit fraction.  positions [M]
  * (8-byte aligned), or NULL: row m has position m % seq_len (m if seq_len is 0).
  * out [M, heads * head_dim] with row stride ldo; it is X itself with ldo = ldx (in
  * place) or does not overlap X.  The backward is the transposed rotation of dY.

@@ -5,9 +5,11 @@
 //
 // Angles are fixed-point turns: theta_i / 2 pi is a 64-bit fraction, and position
 // times it modulo 2^64 is one integer multiply whose wrap-around drops the whole
-// turns exactly.  A position p is off by p 2^-65 turns at most (2^-34 at p = 2^31),
-// where a binary32 product would be off by whole radians; no 64-bit floating point
-// and no table of cosines per position is needed.
+// turns exactly.  The 32 upper bits become a binary32 number: 2^-32 turns dropped and
+// 2^-26 rounded at most (half a turn has 24 bits), the same at every position, where
+// a binary32 product would be off by whole radians at far ones.  An entry of the
+// table counts p times: p 2^-65 turns where it is the nearest fraction.  No 64-bit
+// floating point and no table of cosines per position is needed.
 //
 // HBM-bound.  A CTA takes one or two tokens: its threads find each token's cosines
 // and sines once (shared memory) while their first loads are on the way, then

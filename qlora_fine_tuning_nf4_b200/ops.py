@@ -1004,7 +1004,10 @@ def rope_frequencies(rot, base=10000.0, scaling=None):
 
 
 def rope_plan(rot, base=10000.0, scaling=None, device="cuda"):
-    """RopePlan of `rope_frequencies(rot, base, scaling)` on the GPU; made once per model."""
+    """RopePlan of `rope_frequencies(rot, base, scaling)` on the GPU; made once per model.
+
+    The frequencies are binary64 numbers, so an entry is off by (ln(base) + 4) 2^-53 of itself and half a unit of 2^-64
+    turns: at position 2^20 that is below 2^-34 turns, at 2^31 about 2^-24 for the fastest pairs."""
     freq, factor = rope_frequencies(rot, base, scaling)
     bits = []
     for w in freq:
