@@ -59,7 +59,7 @@ cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, f
 cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st);
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
-                        int64_t ldo, cudaStream_t st);
+                        int64_t ldo, int sms, cudaStream_t st);
 extern const uint32_t h_nf4_bits[16];
 int g_grid_cap = 0;
 }  // namespace ql
@@ -1398,7 +1398,7 @@ static qlora_status rope(const qlora_bf16* X, int64_t M, int64_t ldx, int32_t he
   KScope k(K_ROPE, st);
   return cuda_status(launch_rope(reinterpret_cast<const bf16*>(X), M, ldx, heads, head_dim, turns, rot,
                                  interleaved != 0, factor, transpose, positions, seq_len, reinterpret_cast<bf16*>(out),
-                                 ldo, st));
+                                 ldo, num_sms(), st));
 }
 qlora_status qlora_rope_fwd(const qlora_bf16* X, int64_t M, int64_t ldx, int32_t heads, int32_t head_dim,
                             const uint64_t* turns, int32_t rot, int32_t interleaved, float factor,

@@ -161,9 +161,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, 16) rope_kernel(const RopeArgs a
 
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
-                        int64_t ldo, cudaStream_t st) {
+                        int64_t ldo, int sms, cudaStream_t st) {
   RopeArgs a = {X, out, turns, pos, ldx, ldo, seq_len, (int)M, heads, D, rot, 1, factor, transpose ? -1.f : 1.f};
-  a.tok = M >= 4 * 148 * ROPE_TOK ? ROPE_TOK : 1;
+  // Tokens per CTA, one against two (us, 148 SMs): 40 heads of 128, 148 rows 3.2 / 4.3, 592 4.2 / 4.9, 1776 8.9 / 7.6,
+  // 8192 29.0 / 30.0; 12 interleaved heads of 96 with 64 rotated, 592 rows 2.5 / 2.8, 1776 4.3 / 3.5, 8192 11.9 / 9.6; 6
+  // heads of 64, 592 rows 2.1 / 2.0, 8192 9.0 / 6.0.  With few rows one token spreads the heads over more CTAs; from
+  // eight rows per SM on two halve the CTAs to set up, which narrow rows gain from and wide ones hardly notice.
+  a.tok = M >= int64_t{8} * sms ? ROPE_TOK : 1;
   const unsigned grid = static_cast<unsigned>((M + a.tok - 1) / a.tok);
 #define QL_ROPE(I_, V_) launch_pdl(rope_kernel<I_, V_>, dim3(grid), dim3(ROPE_THREADS), 0, st, a)
   // the widest vector that divides the rotated part: heads start on 16 bytes (D % 8 == 0)
