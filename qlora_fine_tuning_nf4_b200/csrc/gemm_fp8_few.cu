@@ -10,8 +10,8 @@
 //   warp 1       TMEM allocation; issues tcgen05.mma, a fresh accumulator per block
 //   warp 2       scales: sa * sw of a block's rows into a shared-memory ring
 //   warps 4-7    accumulate: TMEM -> scale -> registers
-// Eight accumulators of 16 to 64 columns hide the way from the MMA to the accumulating
-// warps and back.  The CTAs' sums meet through distributed shared memory, are added in
+// Eight accumulators of 16 or 32 columns (four of 64) hide the way from the MMA to the
+// accumulating warps and back.  The CTAs' sums meet through distributed shared memory, are added in
 // rank order and leave as bf16.  The LoRA term is two more blocks of the last CTA, the
 // halves of the low-rank pair (gemm_fp8.cu): bf16 operands (kind::f16) and scale 1.
 //
@@ -56,15 +56,6 @@ struct FewArgs {
   bf16* out;          // [M, cols]
   int* status;
 };
-
-QL_DEV float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 template <bool BWD, int NT>
 __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
