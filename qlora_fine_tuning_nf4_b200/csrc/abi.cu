@@ -47,16 +47,17 @@ cudaError_t launch_fp8_quantize_rows(const bf16* X, int64_t M, int64_t K, uint8_
 cudaError_t launch_fp8_quantize(const bf16* w, int64_t N, int64_t K, uint8_t* codes, float* scale, cudaStream_t st);
 cudaError_t launch_gemm_fp8(bool bwd, int bn, const Gemm8Maps& maps, const Gemm8Args& args, cudaStream_t stream);
 cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
-                                cudaStream_t st);
+                                int* status, cudaStream_t st);
 int gemm_fp8_few_rows(int64_t M);
 cudaError_t launch_gemm_fp8_few(bool bwd, const FewMaps& maps, const float* sa, const float* sb, int sb_k, int sb_n,
                                 int M, int red, int cols, int cluster, int r, bf16* out, int* status,
                                 cudaStream_t st);
 cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
-                            bf16* low, bf16* lows, int sms, cudaStream_t st);
+                            bf16* low, bf16* lows, int sms, int* status, cudaStream_t st);
 cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
-                           bf16* lows, const bf16* XA, bf16* dB, int sms, cudaStream_t st);
-cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st);
+                           bf16* lows, const bf16* XA, bf16* dB, int sms, int* status, cudaStream_t st);
+cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, int* status,
+                           cudaStream_t st);
 cudaError_t launch_rope(const bf16* X, int64_t M, int64_t ldx, int heads, int D, const uint64_t* turns, int rot,
                         bool interleaved, float factor, bool transpose, const int64_t* pos, int64_t seq_len, bf16* out,
                         int64_t ldo, int sms, cudaStream_t st);
@@ -1545,7 +1546,7 @@ qlora_status gemm_fp8(bool bwd, const uint8_t* codes, const float* scale, const 
     if (s != QLORA_OK || plan.splits == 1) return s;
   }
   KScope k(K_GEMM8_SUM, st);
-  return cuda_status(launch_gemm_fp8_sum(part, prows, plan.splits, M, out, D, st));
+  return cuda_status(launch_gemm_fp8_sum(part, prows, plan.splits, M, out, D, status, st));
 }
 
 qlora_status fp8_matmul_any(bool bwd, const qlora_fp8_rows* x, const qlora_fp8* w, int64_t M, qlora_bf16* out,
@@ -1652,7 +1653,7 @@ qlora_status qlora_linear8_fwd(const qlora_lora_linear8* lin, const qlora_bf16* 
                                       reinterpret_cast<const bf16*>(lin->A), r, lin->scale,
                                       X8 ? nullptr : reinterpret_cast<uint8_t*>(w + l.codes),
                                       reinterpret_cast<float*>(w + l.scale), reinterpret_cast<bf16*>(XA_saved), XAs,
-                                      num_sms(), st));
+                                      num_sms(), status, st));
     }
     if (s != QLORA_OK) return s;
     return gemm_fp8(false, codes, scale, lin->w, M, reinterpret_cast<bf16*>(Y), XAs,
@@ -1706,14 +1707,15 @@ qlora_status qlora_linear8_bwd(const qlora_lora_linear8* lin, const qlora_bf16* 
     {
       KScope k(K_PASS8, st);
       s = cuda_status(launch_pass_dy(dy, (int)M, (int)N, reinterpret_cast<const bf16*>(lin->B), r, sc, codes, scale, sG,
-                                     xa, reinterpret_cast<bf16*>(dB), num_sms(), st));
+                                     xa, reinterpret_cast<bf16*>(dB), num_sms(), status, st));
     }
     if (s != QLORA_OK) return s;
     s = gemm_fp8(true, codes, scale, lin->w, M, reinterpret_cast<bf16*>(dX), sG,
                  reinterpret_cast<const bf16*>(lin->A), r, part, status, st);
     if (s != QLORA_OK) return s;
     KScope k(K_PASS8, st);
-    return cuda_status(launch_pass_da(x, (int)M, (int)K, sG, r, reinterpret_cast<bf16*>(dA), num_sms(), st));
+    return cuda_status(launch_pass_da(x, (int)M, (int)K, sG, r, reinterpret_cast<bf16*>(dA), num_sms(), status,
+                                      st));
   }
   if ((s = fp8_quantize_rows(dY, M, N, codes, scale, stream)) != QLORA_OK) return s;
   const ReduceOuts gouts = routs(rout(sG, 0, r, 2 * r, 0, sc), rout(sG + r, 0, r, 2 * r, 0, sc, 1));

@@ -52,6 +52,7 @@ struct RankPass {
   bf16* outer;       // dB [r, C] (scaled) or dA [C, r]
   float scale;
   int cluster;       // CTAs per 64 rows
+  int* status;       // device status word (the checked build's checks report there)
 };
 
 QL_DEV void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -74,6 +75,11 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_rank_pass_kernel(const RankPas
   const bf16* T = a.T + static_cast<size_t>(m0) * a.C;
   grid_dep_wait();
   grid_dep_launch();
+  if (!dev_check(M > 0 && a.C > 0 && (r == 16 || r == 32 || r == 64) && (MODE == PASS_FWD || a.M <= FW_ROWS) &&
+                     (MODE == PASS_DA || a.cluster <= 16) &&
+                     static_cast<int>(gridDim.x) == (a.M + FW_ROWS - 1) / FW_ROWS * a.cluster,
+                 a.status))
+    return;
 
   // block kb of T (rows past M and columns past C as zeros) and of V into buffer b
   auto stage = [&](int kb, int b) {
@@ -367,19 +373,20 @@ static cudaError_t launch_pass(RankPass a, int sms, cudaStream_t st) {
 
 // q(X) and XA (low), the pair of s XA (lows)
 cudaError_t launch_pass_fwd(const bf16* X, int M, int K, const bf16* A, int r, float scale, uint8_t* codes, float* tscale,
-                            bf16* low, bf16* lows, int sms, cudaStream_t st) {
-  return launch_pass<PASS_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale, 1}, sms, st);
+                            bf16* low, bf16* lows, int sms, int* status, cudaStream_t st) {
+  return launch_pass<PASS_FWD>({X, M, K, r, codes, tscale, A, low, lows, nullptr, nullptr, scale, 1, status}, sms, st);
 }
 // q(dY), the pair of s G (lows) and dB = s XA^T dY, M <= 64
 cudaError_t launch_pass_dy(const bf16* dY, int M, int N, const bf16* B, int r, float scale, uint8_t* codes, float* tscale,
-                           bf16* lows, const bf16* XA, bf16* dB, int sms, cudaStream_t st) {
+                           bf16* lows, const bf16* XA, bf16* dB, int sms, int* status, cudaStream_t st) {
   if (M > FW_ROWS) return cudaErrorInvalidValue;
-  return launch_pass<PASS_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale, 1}, sms, st);
+  return launch_pass<PASS_DY>({dY, M, N, r, codes, tscale, B, nullptr, lows, XA, dB, scale, 1, status}, sms, st);
 }
 // dA = X^T (s G) from the pair of s G, M <= 64
-cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, cudaStream_t st) {
+cudaError_t launch_pass_da(const bf16* X, int M, int K, const bf16* sG, int r, bf16* dA, int sms, int* status,
+                           cudaStream_t st) {
   if (M > FW_ROWS) return cudaErrorInvalidValue;
-  return launch_pass<PASS_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f, 1}, sms, st);
+  return launch_pass<PASS_DA>({X, M, K, r, nullptr, nullptr, nullptr, nullptr, nullptr, sG, dA, 1.f, 1, status}, sms, st);
 }
 
 }  // namespace ql

@@ -434,11 +434,12 @@ static cudaError_t launch_one8(const Gemm8Maps& maps, const Gemm8Args& args, cud
 
 // out[m, n] = sum of the parts in order; eight columns per thread.
 __global__ void __launch_bounds__(256) gemm_fp8_sum_kernel(const float* __restrict__ part, int64_t prows, int splits,
-                                                           int64_t N, int64_t total, bf16* __restrict__ out) {
+                                                           int64_t N, int64_t total, bf16* __restrict__ out,
+                                                           int* status) {
   grid_dep_wait();
   grid_dep_launch();
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= total) return;
+  if (i >= total || !dev_check(splits > 1 && i + 8 <= total && total <= prows * N, status)) return;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) {
@@ -451,9 +452,9 @@ __global__ void __launch_bounds__(256) gemm_fp8_sum_kernel(const float* __restri
                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 cudaError_t launch_gemm_fp8_sum(const float* part, int64_t prows, int splits, int64_t M, int64_t N, bf16* out,
-                                cudaStream_t st) {
+                                int* status, cudaStream_t st) {
   return launch_pdl(gemm_fp8_sum_kernel, dim3(static_cast<unsigned>((M * N / 8 + 255) / 256)), dim3(256), 0, st, part,
-                    prows, splits, N, M * N, out);
+                    prows, splits, N, M * N, out, status);
 }
 
 // bn: output columns per tile (256 or 128); the tensor maps' boxes follow it.

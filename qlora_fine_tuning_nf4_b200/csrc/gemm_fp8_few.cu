@@ -70,6 +70,14 @@ __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
   const int own = (a.nkb - rank + a.cluster - 1) / a.cluster;  // blocks rank, rank + cluster, ...
   const int mine = own + (a.lora_k16 > 0 && rank == a.cluster - 1 ? 2 : 0);
 
+  if (!dev_check(a.M > 0 && a.M <= NT && a.cols > 0 && a.cluster >= 1 && a.cluster <= 8 && a.nkb >= a.cluster &&
+                     a.lora_k16 >= 0 && a.lora_k16 <= 4 &&
+                     static_cast<int>(gridDim.x) == (a.cols + C::BM - 1) / C::BM * a.cluster,
+                 a.status)) {
+    grid_dep_wait();
+    return;
+  }
+
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::S + s); };
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::THREADS, 2)
   // each CTA finishes every cluster-th row, four columns per thread (cols % 16 == 0)
   for (int i = threadIdx.x; i < (a.M - rank + a.cluster - 1) / a.cluster * (C::BM / 4); i += C::THREADS) {
     const int m = rank + i / (C::BM / 4) * a.cluster, c = i % (C::BM / 4) * 4, n = n0 + c;
-    if (n >= a.cols) continue;
+    if (n >= a.cols || !dev_check(m < a.M && n + 4 <= a.cols, a.status)) continue;
     float4 x[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p)
