@@ -400,7 +400,7 @@ def _dims(lin):
 _growth_streams = {}  # device index -> stream on which buffers are zeroed while the current stream is being captured
 
 
-def _zeroed_outside_capture(nbytes, device):
+def _zeroed_outside_capture(nbytes):
     """Zeroed bytes while the current stream is being captured.  Made there they would belong to the graph: zeroed by
     each of its replays (with the status word in them) and by nothing before the first one, in memory that other
     graphs of the pool write to.  So they are made on a stream that is not captured, and zero on return.  A thread
@@ -415,7 +415,7 @@ def _zeroed_outside_capture(nbytes, device):
         if dev not in _growth_streams:
             _growth_streams[dev] = torch.cuda.Stream()
         with torch.cuda.stream(_growth_streams[dev]):
-            buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
         _growth_streams[dev].synchronize()
     finally:
         exchange(ctypes.byref(mode))
@@ -436,9 +436,10 @@ class Workspace:
         self._make(256)
 
     def _make(self, nbytes):
-        self.apart = bool(_capturing())  # made on a stream of its own
-        self.buf = (_zeroed_outside_capture(nbytes, self.device) if self.apart
-                    else torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
+        with torch.cuda.device(self.device):  # its current stream counts, where the buffer is made on another device
+            self.apart = bool(_capturing())   # made on a stream of its own
+            self.buf = (_zeroed_outside_capture(nbytes) if self.apart
+                        else torch.zeros(nbytes, dtype=torch.uint8, device="cuda"))
 
     def get(self, nbytes):
         if self.buf.get_device() != _current_device():
