@@ -2,12 +2,11 @@
 //   forward   q(X), XA = X A                       (PASS_FWD, any M)
 //   backward  q(dY), G = dY B^T, dB = s XA^T dY    (PASS_DY, M <= 64)
 //             dA = X^T (s G)                       (PASS_DA, M <= 64)
-// s X A and s G leave as pairs of bf16 numbers (the rounded sum and what the rounding
-// leaves, 16 bits together) for the products that go on from them.
 // each in one launch that reads T once, for the row counts that launches bound: the
 // general path runs a quantiser, one or two passes with fp32 partials and a reduction
-// for each of them (64 rows, rank 64, 4096 -> 1024: 12 launches a step, 44 us; here 6,
-// 33 us).
+// for each of them (64 rows, rank 64, 4096 -> 1024: 12 launches a step, 44 us; here 5,
+// 32 us).  s X A and s G leave as pairs of bf16 numbers (the rounded sum and what the
+// rounding leaves, 16 bits together) for the products that go on from them.
 //
 // A cluster takes 64 rows.  T comes in blocks of 128 columns, staged in shared
 // memory together with the low-rank factor's block (the next blocks' copies are on

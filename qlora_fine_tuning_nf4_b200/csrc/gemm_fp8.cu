@@ -25,9 +25,11 @@
 //
 // What bounds it.  Per block and SM the tensor core needs 512 cycles, 32 KB come
 // from L2 (64 bytes a cycle: 512 as well), and the accumulating warps 256 cycles
-// of fma and as many of TMEM loads per scheduler.  8192 x 4096 x 11008 takes 0.31
-// ms (2.36 PFLOP/s); the same kernel without the scaling, adding the blocks in
-// TMEM, 0.24 ms.  On the way there, each measured on that product:
+// of fma and as many of TMEM loads per scheduler.  8192 x 4096 x 11008 takes 0.30
+// to 0.35 ms in bursts of ten (2.1 to 2.4 PFLOP/s, by the box) and 0.37 ms (2.0) in a
+// long run of calls, under the 1 kW power cap; the same kernel without the scaling,
+// adding the blocks in TMEM, 0.24 ms where this one took 0.31.  On the way there, each
+// measured on that product:
 //  * issuing from one elected thread of a converged warp (elect.sync) instead of
 //    under `lane == 0`: 0.39 -> 0.35 ms.  Under a divergent branch every MMA,
 //    commit and TMA load costs tens of cycles more, and the issue loop is one

@@ -16,7 +16,8 @@
 // halves of the low-rank pair (gemm_fp8.cu): bf16 operands (kind::f16) and scale 1.
 //
 // With weights that come from HBM: one row, 4096 -> 14336 (59 MB, 9.1 us at the copy
-// rate) 12.9 us, 4096 -> 4096 (17 MB, 2.6 us) 6.5 us; 64 rows 16.2 and 8.5 us.  Warp-level
+// rate) 13.1 us, 4096 -> 4096 (17 MB, 2.6 us) 6.6 us; 64 rows 15.9 and 8.3 us; dX of the
+// same weights 13.3 and 6.7, 17.1 and 8.6 us.  Warp-level
 // MMAs fed by the same ring of TMA loads took 17.5 us for the former: an e4m3
 // m16n8k32 occupies a scheduler for about 64 cycles, so they were bound by it.  Stages
 // for two CTAs per SM rather than one: the next CTA (or the next launch's) sets up
