@@ -1587,7 +1587,9 @@ constexpr int64_t kOnePassRows = 64, kFwdPassRows = 256;
 // Workspace of an e4m3 projection: [status word | 256 B][M x 2r: the pair of s XA or s G][row codes][row
 // scales][partials].  The pair (the bf16 rounding of an fp32 sum, and what it leaves) carries the sum to 2^-16
 // of it into Y, dX and dA: one rounding alone gave dA sqrt(2) of the error that its own rounding has.  It costs
-// one more block per product and twice the columns of the dA pass.
+// one more block per product and twice the columns of the dA pass: 1 to 6% of a step (2048 x 4096 -> 4096, rank
+// 16 108.4 -> 109.7 us; 4096 x 4096 -> 4096, rank 64 225 -> 237 us).  XA_saved, an activation that the caller
+// keeps, is bf16 like the others; dB starts from it.
 // At ranks 32 and 64 the backward reduces its dB and dA passes in one launch at the end, so their
 // partials stay apart from those of the passes between: [dB][dA][the rest].
 struct Linear8Ws {
